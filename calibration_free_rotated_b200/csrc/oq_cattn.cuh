@@ -1,0 +1,232 @@
+// What the two attention kernels over the 8-bit cache share: how the work is
+// shared out, and how the pieces of a split row are put together.
+//
+// An item is (sequence, head of the cache, tile of query rows): the rows of a
+// tile are the new tokens' query heads that share the cache's head, row r being
+// token r / group, head r % group of the group.  An item's work is its number of
+// key tiles.  The items' tiles in a row (sequence, head, row tile) are cut into
+// equal shares, one for each CTA, wherever the cut falls, so that ragged batches
+// and a single long stream fill the machine alike.  A CTA finds its share from
+// the lengths on the device: nothing about them is known on the host.
+//
+// An item that one CTA covers is finished there.  Of an item that is cut, each
+// CTA leaves a piece in the workspace (for each row its running maximum, sum and
+// weighted values, fp32): the CTA that begins it in its slot 1, the ones that go
+// on with it in their slot 0.  The beginning CTA also writes down which CTAs hold
+// pieces, and the joining kernel adds them up in the CTAs' order: no atomics, the
+// same result every time.
+#pragma once
+
+#include "oq_cache.cuh"
+
+namespace oq {
+namespace cattn {
+
+using namespace cache;
+
+constexpr int kTile = 64;  // keys of a tile: the unit of work
+
+struct Args {
+  View c;
+  Rotation r;
+  const void* q;
+  void* out;
+  long long qt, qh, ot, oh;  // strides in elements
+  const int* cu;
+  const int* lens;
+  const int* table;
+  int* status;
+  float* piece;   // [2 ctas][rows of a tile][D]
+  float* stat;    // [2 ctas][rows of a tile][2]: maximum, sum
+  int4* desc;     // [ctas]: (pieces, sequence, head, row tile)
+  int B, T, width, group, causal;
+  float scale;    // of the scores, times log2(e)
+};
+
+// Lengths of one sequence; rows = 0 where its numbers do not fit (reported) or it has no new token.
+struct Seq {
+  int cu0, n, len, rows;
+};
+__device__ __forceinline__ Seq load_seq(const Args& a, int b, bool report) {
+  Seq s;
+  s.cu0 = a.cu[b];
+  s.n = a.cu[b + 1] - s.cu0;
+  s.len = a.lens[b];
+  const bool ok = s.cu0 >= 0 && s.n >= 0 && s.cu0 + (long long)s.n <= a.T && s.len >= 0 &&
+                  s.len <= (long long)a.width * a.c.page;
+  if (!ok) {
+    if (report) bad_index(a.status);
+    s.n = 0;
+  }
+  s.rows = s.n * a.group;
+  return s;
+}
+// Keys that the row tile's last row may see (causal: the tile's other rows see no more).
+template <int RT>
+__device__ __forceinline__ int tile_keys(const Args& a, const Seq& s, int qt) {
+  if (!a.causal) return s.len;
+  const int last = min(s.rows - 1, qt * RT + RT - 1) / a.group;
+  return max(0, s.len - s.n + last + 1);
+}
+template <int RT>
+__device__ __forceinline__ int tile_work(const Args& a, const Seq& s, int qt) {
+  return max(1, (tile_keys<RT>(a, s, qt) + kTile - 1) / kTile);
+}
+template <int RT>
+__device__ __forceinline__ long long head_work(const Args& a, const Seq& s) {
+  const int tiles = (s.rows + RT - 1) / RT;
+  if (!a.causal || tiles <= 1) return tiles ? (long long)tiles * tile_work<RT>(a, s, 0) : 0;
+  long long w = 0;
+  for (int qt = 0; qt < tiles; ++qt) w += tile_work<RT>(a, s, qt);
+  return w;
+}
+
+// Where a CTA's share begins.
+struct Share {
+  long long total, size;  // tiles of all items, of a share
+  int b;                  // sequence of the first tile; B when the share is empty
+  long long into;         // tiles of that sequence before it
+};
+
+// All THREADS threads of the CTA take part and get the same answer.
+template <int RT, int THREADS>
+__device__ Share find_share(const Args& a, int cta, int ctas) {
+  __shared__ long long warp_sum[THREADS / 32];
+  __shared__ Share found;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long total = 0, mine = 0, start = 0, size = 0;
+  if (threadIdx.x == 0) found.b = a.B;
+  // two passes over the sequences: the sum, then the one that holds the start;
+  // up to THREADS of them need their lengths only once
+  for (int pass = 0; pass < 2; ++pass) {
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+      const int b = b0 + (int)threadIdx.x;
+      if (pass == 0 || a.B > THREADS) {
+        mine = 0;
+        if (b < a.B) {
+          const Seq s = load_seq(a, b, pass == 0 && cta == 0);
+          mine = head_work<RT>(a, s) * a.c.heads;
+        }
+      }
+      long long incl = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+        if (lane >= m) incl += o;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      long long base = before;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += warp_sum[w];
+        before += warp_sum[w];
+      }
+      if (pass == 1) {
+        const long long first = base + incl - mine;
+        if (start >= first && start < first + mine) {
+          found.b = b;
+          found.into = start - first;
+        }
+      }
+      __syncthreads();
+    }
+    total = before;
+    size = (total + ctas - 1) / ctas;
+    start = size * cta;
+  }
+  Share s = found;
+  s.total = total, s.size = size;
+  return s;
+}
+
+// Puts the pieces of cut items together and writes their rows: block (i, j) the
+// rows j, j + gridDim.y, ... of the item that CTA i began.
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a, int pdl) {
+  __shared__ float part[4][D];
+  __shared__ float part_sum[4], part_max[4];
+  __shared__ __align__(16) T row_out[D];
+  if (pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 d = a.desc[blockIdx.x];
+  if (d.x <= 0) return;
+  const Seq s = load_seq(a, d.y, false);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = min(RT, s.rows - d.w * RT);
+  constexpr int V = D / 32;  // values of a lane
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * RT + r; };
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < d.x; i += 128) top = fmaxf(top, a.stat[2 * slot(i)]);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+    if (lane == 0) part_max[warp] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(part_max[0], part_max[1]), fmaxf(part_max[2], part_max[3]));
+    if (top == -INFINITY) top = 0.0f;
+    float o[V], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = 0.0f;
+#pragma unroll 4
+    for (int i = warp; i < d.x; i += 4) {
+      const size_t at = slot(i);
+      const float f = exp2f(a.stat[2 * at] - top);
+      sum = fmaf(f, a.stat[2 * at + 1], sum);
+      const float* p = a.piece + at * D + V * lane;
+      if constexpr (V == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]), o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) part[warp][V * lane + k] = o[k];
+    if (lane == 0) part_sum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      sum = part_sum[0] + part_sum[1] + part_sum[2] + part_sum[3];
+      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // no key: 0; NaN stays
+      const int l = lane % (D / 8);
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[k] = ((part[0][8 * l + k] + part[1][8 * l + k]) + (part[2][8 * l + k] + part[3][8 * l + k])) * inv;
+      uint4 w;
+      if (a.r.perm) {
+        unrotate_row<T>(x, lane_turn(a.r, l), l, a.r, row_out);  // lanes of one l write the same values
+        __syncwarp();
+        w = *reinterpret_cast<const uint4*>(row_out + 8 * l);
+      } else {
+        w = pack8<T>(x);
+      }
+      const int g = d.w * RT + r, i = g / a.group;
+      if (lane < D / 8)
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
+                                  ((long long)d.z * a.group + (g - i * a.group)) * a.oh + 8 * l) = w;
+    }
+    __syncthreads();
+  }
+}
+
+// Registers of four signed codes (bytes of w) as two fp16 pairs: a byte with its
+// sign bit turned is code + 128, the low byte of the fp16 number 1024 + code + 128.
+__device__ __forceinline__ uint32_t sub_bias(uint32_t h) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+  return r;
+}
+__device__ __forceinline__ uint32_t bytes2(uint32_t biased, uint32_t sel) {
+  return sub_bias(__byte_perm(biased, 0x64646464u, sel));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+}  // namespace cattn
+}  // namespace oq

@@ -17,8 +17,6 @@
 #include <new>
 #include <string>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "oq_internal.h"
 
 namespace oq {
@@ -283,6 +281,11 @@ static cudaError_t dev_malloc(void** p, size_t bytes) {
   cudaError_t e = cudaMalloc(p, bytes);
   if (e == cudaSuccess) g_dev_allocs.fetch_add(1, std::memory_order_relaxed);
   return e;
+}
+
+int device_alloc(void** p, size_t bytes, const char* what) {
+  cudaError_t e = dev_malloc(p, bytes);
+  return e == cudaSuccess ? OQ_OK : fail(OQ_ERR_CUDA, "cudaMalloc(%s): %s", what, cudaGetErrorString(e));
 }
 
 static std::mutex g_dev_mu;
@@ -695,15 +698,6 @@ int rpbh_device_tables(oq_rpbh_t r, const uint16_t** perm, const uint32_t** sign
   return OQ_OK;
 }
 
-// Host span of an entry point for timeline tools (NVTX; a no-op unless a tool
-// such as ncu --nvtx is attached).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
 static std::atomic<int> g_test_stall{0};
 
 int take_test_stall(int kernel) {
@@ -794,11 +788,7 @@ static int make_rotation(uint64_t seed, int d, int block, int kind, int rounds, 
 // ===========================================================================
 using namespace oq;
 
-extern "C" {
-
-int oq_version(void) { return OQ_VERSION; }
-
-long long oq_device_allocations(void) { return g_dev_allocs.load(std::memory_order_relaxed); }
+namespace oq {
 
 // Synchronous checking (OQ_DEBUG=1 in the environment, or oq_set_debug): each
 // launching entry point then waits for its stream and returns the device status
@@ -818,10 +808,18 @@ static bool debug_on() {
   return v != 0;
 }
 
-static int finish(int rc, void* stream) {
+int finish(int rc, void* stream) {
   if (rc != OQ_OK || !debug_on()) return rc;
   return oq_get_device_status(stream);
 }
+
+}  // namespace oq
+
+extern "C" {
+
+int oq_version(void) { return OQ_VERSION; }
+
+long long oq_device_allocations(void) { return g_dev_allocs.load(std::memory_order_relaxed); }
 
 int oq_set_debug(int on) {
   clear_error();
@@ -866,6 +864,8 @@ int oq_get_device_status(void* stream) {
   e = cudaMemcpy(&v, st, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemset(st, 0, sizeof(int));
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "reading device status: %s", cudaGetErrorString(e));
+  if (v == OQ_ERR_ARG)
+    return fail(v, "a kernel met an index out of range in device memory (a page, a length or a row offset)");
   if (v != OQ_OK) return fail(v, "a kernel reported device status %d (bounded wait gave up)", v);
   return OQ_OK;
 }

@@ -6,6 +6,8 @@
 #include <mutex>
 #include <vector>
 
+#include <nvtx3/nvToolsExt.h>
+
 #include "../../include/orbitquant.h"
 
 #define OQ_MAX_DEVICES 64
@@ -45,7 +47,32 @@ struct oq_codebook_s {
   uint32_t* dev_qtable[OQ_MAX_DEVICES] = {};
 };
 
+// Rotary frequencies: pair p turns by freq[p] (a 64-bit fraction of a turn) for
+// each position on axis axis[p].
+struct oq_rope_s {
+  int n_axes = 0, halves = 0;
+  std::vector<uint64_t> freq;
+  std::vector<uint8_t> axis;
+  std::mutex mu;
+  unsigned char* dev_table[OQ_MAX_DEVICES] = {};  // freq, then axis
+};
+
 namespace oq {
+
+// Host span of an entry point for timeline tools (NVTX; a no-op unless a tool
+// such as ncu --nvtx is attached).
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+  NvtxRange(const NvtxRange&) = delete;
+  NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+// Every device allocation of the library (counted for oq_device_allocations).
+int device_alloc(void** p, size_t bytes, const char* what);
+// The end of a launching entry point: under synchronous checking, waits for the
+// stream and returns the device status.
+int finish(int rc, void* stream);
 
 // Error reporting: store a message for oq_last_error() and return `code`.
 int fail(int code, const char* fmt, ...);
@@ -120,5 +147,45 @@ int launch_flatness(const void* X, int M, int d, float* rho3, float* rhoinf, flo
 int launch_cbgemm(int d, oq_codebook_t cb_a, oq_codebook_t cb_w, const uint8_t* a_codes, const float* a_norm, int M,
                   const uint8_t* w_codes, const uint16_t* w_norm, int N, const uint16_t* bias, int epilogue,
                   float* Y_f32, uint16_t* Y_bf16, void* stream);
+
+// The cache operators.  Arguments are checked by the entry points (oq_cache_host.cpp).
+struct RopeCall {
+  const void* x;
+  void* y;
+  const unsigned long long* freq;
+  const uint8_t* axis;
+  const int* pos;
+  long long x_token, x_head, y_token, y_head;  // strides in elements
+  int dtype, T, heads, d, n_axes, pairs, halves, inverse;
+  void* stream;
+};
+struct CacheCall {
+  const oq_kvcache* cache;
+  oq_rpbh_t r;  // or nullptr
+  const void *k, *v;    // write
+  void *k_out, *v_out;  // read
+  long long k_token, k_head, v_token, v_head;
+  int dtype, B, T, width;
+  const int *cu, *at, *table;
+  void* stream;
+};
+struct AttnCall {
+  const oq_kvcache* cache;
+  oq_rpbh_t r;  // or nullptr
+  const void* q;
+  void* out;
+  long long q_token, q_head, o_token, o_head;
+  int dtype, heads, B, T, width, causal;
+  float scale;
+  const int *cu, *lens, *table;
+  void* workspace;
+  void* stream;
+};
+int cache_rotation(oq_rpbh_t r, void* rotation);  // fills a cache::Rotation
+int launch_rope(const RopeCall& c);
+int launch_cache_write(const CacheCall& c);
+int launch_cache_read(const CacheCall& c);
+int launch_cattn(const AttnCall& c);
+size_t cattn_workspace(int T, int B, int group, int d);
 
 }  // namespace oq

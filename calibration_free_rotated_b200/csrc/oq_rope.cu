@@ -1,0 +1,192 @@
+// Rotary positions over several axes.
+//
+// Pair p of a head turns by phi = pos[t][axis_p] * f_p:
+//   (a, b) -> (a cos phi - b sin phi, a sin phi + b cos phi)
+// (the transposed turn, phi -> -phi, is the inverse and the gradient).
+// The angle is exact for far positions: f_p is held in turns per position as a
+// 64-bit fraction F = round(f_p / 2pi * 2^64), and pos * F mod 2^64 is the
+// turn's fraction with an error below |pos| * 2^-65, reduced without a float
+// division; its top 32 bits go through sincospif.
+//
+// Bound by memory (each value is read and written once).  A CTA takes a few
+// tokens and a share of the heads: its threads first put the tokens' cosines
+// and sines into shared memory (once for all heads), then each thread turns
+// pairs of 16-byte vectors.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "oq_cache.cuh"
+
+namespace oq {
+namespace {
+
+using namespace cache;
+
+constexpr int kThreads = 256;
+
+struct RopeArgs {
+  const char* x;
+  char* y;
+  const unsigned long long* freq;  // [pairs]
+  const uint8_t* axis;             // [pairs]
+  const int* pos;                  // [T][n_axes]
+  long long xt, xh, yt, yh;        // strides in bytes
+  int T, heads, n_axes, pairs, halves, inverse;
+  int tokens, head_share;   // per CTA
+  int units;                // vector pairs of a row
+  unsigned div_units;       // ceil(2^32 / units)
+};
+
+template <typename T>
+struct Vec;  // 16 bytes of T
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void load(uint4 w, float (&x)[8]) { unpack8<__nv_bfloat16>(w, x); }
+  static __device__ __forceinline__ uint4 store(const float (&x)[8]) { return pack8<__nv_bfloat16>(x); }
+};
+template <>
+struct Vec<__half> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void load(uint4 w, float (&x)[8]) { unpack8<__half>(w, x); }
+  static __device__ __forceinline__ uint4 store(const float (&x)[8]) { return pack8<__half>(x); }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void load(uint4 w, float (&x)[4]) {
+    x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 store(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+};
+
+// A row's 16-byte vectors in units of two: HALVES: unit u < pairs / N holds the
+// vectors N u and pairs + N u that turn into each other; otherwise, and for
+// what lies behind the turned part, two neighbouring vectors.  An odd vector at
+// the end stands alone (`two` false).
+template <typename T, bool HALVES>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int vecs) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ float2 turns[];  // [tokens][pairs]
+  const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.T - t0);
+  const int h0 = blockIdx.y * a.head_share, nh = min(a.head_share, a.heads - h0);
+  for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
+    const int t = i / a.pairs, p = i - t * a.pairs;
+    const long long pos = a.pos[(size_t)(t0 + t) * a.n_axes + a.axis[p]];
+    const unsigned long long turn = (unsigned long long)pos * a.freq[p];
+    float s, c;
+    sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
+    turns[i] = make_float2(c, a.inverse ? -s : s);
+  }
+  __syncthreads();
+  const int row_units = a.units, total = nt * nh * row_units;
+  const int first_pass = HALVES ? a.pairs / N : 0;  // units that pair two halves
+  for (int i = threadIdx.x; i < total; i += kThreads) {
+    const int row = row_units == 1 ? i : (int)__umulhi((unsigned)i, a.div_units);
+    const int u = i - row * row_units;
+    const int t = row / nh, h = row - t * nh;
+    const char* x = a.x + (t0 + t) * a.xt + (h0 + h) * a.xh;
+    char* y = a.y + (t0 + t) * a.yt + (h0 + h) * a.yh;
+    const float2* cs = turns + t * a.pairs;
+    if (HALVES && u < first_pass) {
+      const uint4 w0 = *reinterpret_cast<const uint4*>(x + 16 * u);
+      const uint4 w1 = *reinterpret_cast<const uint4*>(x + 16 * (u + first_pass));
+      float p[N], q[N];
+      Vec<T>::load(w0, p);
+      Vec<T>::load(w1, q);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float2 r = cs[u * N + k];
+        const float b = q[k];
+        q[k] = fmaf(p[k], r.y, b * r.x);
+        p[k] = fmaf(p[k], r.x, -(b * r.y));
+      }
+      *reinterpret_cast<uint4*>(y + 16 * u) = Vec<T>::store(p);
+      *reinterpret_cast<uint4*>(y + 16 * (u + first_pass)) = Vec<T>::store(q);
+    } else {
+      const int v0 = 2 * first_pass + 2 * (u - first_pass);
+      const bool two = v0 + 1 < vecs;
+      uint4 w[2];
+      w[0] = *reinterpret_cast<const uint4*>(x + 16 * v0);
+      if (two) w[1] = *reinterpret_cast<const uint4*>(x + 16 * (v0 + 1));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (j == 1 && !two) break;
+        const int p0 = (v0 + j) * (N / 2);
+        if (!HALVES && p0 < a.pairs) {  // the rest is carried over bit for bit
+          float p[N];
+          Vec<T>::load(w[j], p);
+          const uint4 as_is = w[j];
+#pragma unroll
+          for (int k = 0; k < N / 2; ++k) {
+            const float2 r = p0 + k < a.pairs ? cs[p0 + k] : make_float2(1.0f, 0.0f);
+            const float b = p[2 * k + 1];
+            p[2 * k + 1] = fmaf(p[2 * k], r.y, b * r.x);
+            p[2 * k] = fmaf(p[2 * k], r.x, -(b * r.y));
+          }
+          w[j] = Vec<T>::store(p);
+          if (p0 + N / 2 > a.pairs) {  // the turned part ends inside this vector
+            const uint32_t* old = &as_is.x;
+            uint32_t* now = &w[j].x;
+            constexpr int words = (int)(sizeof(T) / 2);  // words of a pair
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k)
+#pragma unroll
+              for (int q = 0; q < words; ++q)
+                if (p0 + k >= a.pairs) now[k * words + q] = old[k * words + q];
+          }
+        }
+        *reinterpret_cast<uint4*>(y + 16 * (v0 + j)) = w[j];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int launch_rope(const RopeCall& c) {
+  RopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const int size = c.dtype == OQ_FP32 ? 4 : 2;
+  a.x = static_cast<const char*>(c.x);
+  a.y = static_cast<char*>(c.y);
+  a.freq = c.freq;
+  a.axis = c.axis;
+  a.pos = c.pos;
+  a.xt = c.x_token * size, a.xh = c.x_head * size, a.yt = c.y_token * size, a.yh = c.y_head * size;
+  a.T = c.T, a.heads = c.heads, a.n_axes = c.n_axes, a.pairs = c.pairs, a.halves = c.halves, a.inverse = c.inverse;
+  const int vecs = c.d * size / 16, n = 16 / size;
+  const int lead = c.halves ? c.pairs / n : 0;
+  a.units = lead + (vecs - 2 * lead + 1) / 2;
+  a.div_units = (unsigned)((0x100000000ull + a.units - 1) / a.units);
+  int nsm;
+  if (int rc = sm_count(&nsm)) return rc;
+  // A CTA turns about 1024 units (four a thread); with few tokens the heads are
+  // shared out so that every SM has work.
+  const int per_token = c.heads * a.units;
+  a.tokens = std::max(1, std::min({1024 / std::max(1, per_token), 16, (c.T + nsm - 1) / nsm}));
+  a.tokens = std::min(a.tokens, 4096 / a.pairs);
+  int blocks = (c.T + a.tokens - 1) / a.tokens;
+  int shares = std::max(1, std::max(std::min(c.heads, (2 * nsm) / blocks), (a.tokens * per_token + 2047) / 2048));
+  shares = std::min(shares, std::min(c.heads, 65535));
+  a.head_share = (c.heads + shares - 1) / shares;
+  const dim3 grid((unsigned)blocks, (unsigned)((c.heads + a.head_share - 1) / a.head_share));
+  const size_t smem = sizeof(float2) * (size_t)a.tokens * a.pairs;
+  cudaStream_t s = (cudaStream_t)c.stream;
+  auto go = [&](auto kern) { kern<<<grid, kThreads, smem, s>>>(a, vecs); };
+  if (c.dtype == OQ_BF16)
+    c.halves ? go(rope_kernel<__nv_bfloat16, true>) : go(rope_kernel<__nv_bfloat16, false>);
+  else if (c.dtype == OQ_FP16)
+    c.halves ? go(rope_kernel<__half, true>) : go(rope_kernel<__half, false>);
+  else
+    c.halves ? go(rope_kernel<float, true>) : go(rope_kernel<float, false>);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
+  return OQ_OK;
+}
+
+}  // namespace oq

@@ -25,7 +25,7 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-_c_int, _c_void_p, _c_size_t = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_c_int, _c_void_p, _c_size_t, _c_i64 = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_longlong
 _SIGS = {
     "oq_version": (_c_int, []),
     "oq_device_allocations": (ctypes.c_longlong, []),
@@ -55,6 +55,19 @@ _SIGS = {
                            _c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
     "oq_linear_noalloc": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_void_p,
                                    _c_int, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p]),
+    "oq_make_rope": (_c_int, [_c_int, _c_void_p, _c_void_p, _c_int, _c_int, ctypes.POINTER(_c_void_p)]),
+    "oq_rope_info": (_c_int, [_c_void_p, ctypes.POINTER(_c_int), ctypes.POINTER(_c_int), ctypes.POINTER(_c_int)]),
+    "oq_free_rope": (None, [_c_void_p]),
+    "oq_rope_apply": (_c_int, [_c_void_p, _c_void_p, _c_i64, _c_i64, _c_void_p, _c_i64, _c_i64, _c_int, _c_int,
+                               _c_int, _c_int, _c_void_p, _c_int, _c_void_p]),
+    "oq_cache_write": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_i64, _c_i64, _c_void_p, _c_i64, _c_i64, _c_int,
+                                _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p]),
+    "oq_cache_read": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p,
+                               _c_int, _c_void_p, _c_int, _c_void_p]),
+    "oq_cache_attention_workspace_bytes": (_c_size_t, [_c_void_p, _c_int, _c_int, _c_int]),
+    "oq_cache_attention": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_i64, _c_i64, _c_void_p, _c_i64, _c_i64,
+                                    _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_int,
+                                    ctypes.c_float, _c_void_p, _c_size_t, _c_void_p]),
     "oq_test_composed_tables": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p]),
 }
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -264,3 +277,224 @@ def linear_noalloc(rpbh: Rpbh, cb_a: Codebook, cb_w: Codebook, X, w_codes, w_nor
                                   N, _ptr(bias), EPILOGUES[epilogue], _ptr(out_f32), _ptr(out_bf16),
                                   _stream(stream)))
     return out_f32, out_bf16
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions, the 8-bit cache, attention over it
+# ---------------------------------------------------------------------------
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # OQ_BF16 ..
+ROPE_LAYOUTS = {"interleaved": 0, "halves": 1}
+
+
+class Rope:
+    """Rotary positions over several axes (oq_make_rope).
+
+    axis_dims: how many of a head's leading elements turn with each axis, in
+    order (even numbers; FLUX heads of 128: (16, 56, 56), Wan's: (44, 42, 42);
+    one axis: (128,)).  With ladder "axis" every axis has frequencies of its
+    own, theta^(-2k / axis_dim) for its pair k; with "shared" the axes share one
+    ladder over all pairs, theta^(-2p / sum(axis_dims)) for pair p.  layout
+    "interleaved" pairs elements 2p and 2p + 1, "halves" p and p + pairs.  Any
+    other frequencies: pass `freqs` and `axes` (one of each for every pair)
+    instead."""
+
+    def __init__(self, axis_dims=None, theta: float = 10000.0, layout: str = "interleaved", ladder: str = "axis",
+                 freqs=None, axes=None):
+        if (axis_dims is None) == (freqs is None) or (freqs is None) != (axes is None):
+            raise ValueError("pass either axis_dims, or freqs and axes")
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"unknown layout {layout!r}")
+        if axis_dims is not None:
+            if ladder not in ("axis", "shared"):
+                raise ValueError(f"unknown ladder {ladder!r}")
+            dims = [int(n) for n in axis_dims]
+            if not dims or any(n < 2 or n % 2 for n in dims):
+                raise ValueError(f"axis_dims must be even and positive (got {dims})")
+            freqs, axes, total = [], [], sum(dims)
+            for a, n in enumerate(dims):
+                for k in range(n // 2):
+                    e = 2 * k / n if ladder == "axis" else 2 * len(freqs) / total
+                    freqs.append(float(theta) ** -e)
+                    axes.append(a)
+            n_axes = len(dims)
+        else:
+            freqs, axes = [float(f) for f in freqs], [int(a) for a in axes]
+            if not freqs or len(freqs) != len(axes) or not all(0 <= a < 256 for a in axes):
+                raise ValueError("freqs and axes need one entry for each pair, axes in 0..255")
+            n_axes = max(axes) + 1
+        n = len(freqs)
+        h = ctypes.c_void_p()
+        _check(_lib.oq_make_rope(n, (ctypes.c_double * n)(*freqs), (ctypes.c_uint8 * n)(*axes), n_axes,
+                                 ROPE_LAYOUTS[layout], ctypes.byref(h)))
+        self._h = h
+        self.pairs, self.n_axes, self.layout = n, n_axes, layout
+
+    @property
+    def handle(self):
+        return self._h
+
+    def __del__(self):
+        h, self._h = getattr(self, "_h", None), None
+        if h and _lib is not None:
+            _lib.oq_free_rope(h)
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("heads", ctypes.c_int),
+                ("page", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class KVCache:
+    """Paged 8-bit cache of keys and values (oq_kvcache): codes k, v int8
+    [n_pages, heads, page, d], scales k_scale, v_scale float32 [n_pages, heads]."""
+
+    def __init__(self, n_pages: int, heads: int, d: int, page: int = 64, device="cuda"):
+        codes = [torch.zeros((n_pages, heads, page, d), dtype=torch.int8, device=device) for _ in range(2)]
+        scales = [torch.zeros((n_pages, heads), dtype=torch.float32, device=device) for _ in range(2)]
+        self._set(*codes, *scales)
+
+    @classmethod
+    def wrap(cls, k, v, k_scale, v_scale):
+        """A cache over tensors that stand already."""
+        c = cls.__new__(cls)
+        c._set(k, v, k_scale, v_scale)
+        return c
+
+    def _set(self, k, v, k_scale, v_scale):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != torch.int8 or v.dtype != torch.int8:
+            raise ValueError("k and v must be int8 [n_pages, heads, page, d]")
+        if tuple(k_scale.shape) != tuple(k.shape[:2]) or k_scale.shape != v_scale.shape or \
+                k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise ValueError("k_scale and v_scale must be float32 [n_pages, heads]")
+        for t in (k, v, k_scale, v_scale):
+            if not t.is_contiguous() or t.device != k.device:
+                raise ValueError("cache tensors must be contiguous and on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.heads, self.page, self.d = k.shape
+        self.device = k.device
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                    self.n_pages, self.heads, self.page, self.d)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device (got {device})")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            rc = fn(*args, s.cuda_stream)
+    else:
+        rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if rc:
+        _check(rc)
+
+
+def _rows(name, t, heads=None, d=None, like=None):
+    """Strides (token, head) of [T, heads, d] rows; checks what the library cannot see."""
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (d is not None and t.shape[2] != d):
+        raise ValueError(f"{name} must be [T, {heads or 'heads'}, {d or 'd'}] (got {tuple(t.shape)})")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if like is not None and (t.shape[0] != like.shape[0] or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must match in tokens, dtype and device (got {tuple(t.shape)}, {t.dtype}, {t.device})")
+    if t.dtype not in DTYPES:
+        raise ValueError(f"{name}: dtype {t.dtype} is not supported")
+    return st, sh
+
+
+def _index(name, t, device, shape):
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or \
+            (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be contiguous int32{'' if shape is None else ' ' + str(list(shape))} on {device} "
+                         f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+    return t.data_ptr()
+
+
+def _batch(cache, cu, at_name, at, table):
+    if at.dim() != 1 or table.dim() != 2 or table.shape[0] != at.shape[0]:
+        raise ValueError(f"{at_name} must be [B] and table [B, width] (got {tuple(at.shape)}, {tuple(table.shape)})")
+    B, dev = at.shape[0], cache.device
+    return (_index("cu", cu, dev, (B + 1,)), _index(at_name, at, dev, None), B, _index("table", table, dev, None),
+            table.shape[1])
+
+
+def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out=None, inverse: bool = False, stream=None):
+    """x: cuda bf16 / fp16 / fp32 [T, heads, d] (rows contiguous, any strides of
+    tokens and heads) turned by pos: int32 [T, axes].  out: written and returned
+    (x itself: in place); a new tensor if None.  inverse: the transposed turn,
+    which is also the gradient."""
+    xt, xh = _rows("x", x)
+    T, heads, d = x.shape
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=x.dtype, device=x.device)
+    ot, oh = _rows("out", out, heads, d, like=x)
+    _launch(_lib.oq_rope_apply, x.device, stream, rope.handle, x.data_ptr(), xt, xh, out.data_ptr(), ot, oh,
+            DTYPES[x.dtype], T, heads, d, _index("pos", pos, x.device, (T, rope.n_axes)), inverse)
+    return out
+
+
+def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, past: torch.Tensor,
+                table: torch.Tensor, rpbh: Rpbh = None, stream=None):
+    """Quantizes the rows k, v (cuda bf16 / fp16 [T, heads, d], rows cu[b] ..
+    cu[b+1]-1 are sequence b's) into the cache behind the past[b] tokens that
+    the sequence holds, in the pages of table: int32 [B, width]."""
+    kt, kh = _rows("k", k, cache.heads, cache.d)
+    vt, vh = _rows("v", v, cache.heads, cache.d, like=k)
+    if k.device != cache.device:
+        raise ValueError(f"k and v must be on the cache's device {cache.device}")
+    cu_p, at_p, B, table_p, width = _batch(cache, cu, "past", past, table)
+    _launch(_lib.oq_cache_write, cache.device, stream, cache._ref, None if rpbh is None else rpbh.handle, k.data_ptr(),
+            kt, kh, v.data_ptr(), vt, vh, DTYPES[k.dtype], k.shape[0], cu_p, at_p, B, table_p, width)
+
+
+def cache_read(cache: KVCache, cu: torch.Tensor, first: torch.Tensor, table: torch.Tensor, T: int = None,
+               rpbh: Rpbh = None, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """Reads tokens first[b] .. of every sequence b back into rows cu[b] ..
+    cu[b+1]-1 of k and v ([T, heads, d] contiguous; made as `dtype` if not
+    passed, with T rows)."""
+    if (k is None) != (v is None) or (k is None and T is None):
+        raise ValueError("pass k and v, or T")
+    if k is None:
+        k, v = (torch.empty((T, cache.heads, cache.d), dtype=dtype, device=cache.device) for _ in range(2))
+    _rows("k", k, cache.heads, cache.d)
+    _rows("v", v, cache.heads, cache.d, like=k)
+    if not k.is_contiguous() or not v.is_contiguous() or k.device != cache.device or (T is not None and T != k.shape[0]):
+        raise ValueError("k and v must be contiguous, of T rows, on the cache's device")
+    cu_p, at_p, B, table_p, width = _batch(cache, cu, "first", first, table)
+    _launch(_lib.oq_cache_read, cache.device, stream, cache._ref, None if rpbh is None else rpbh.handle, k.data_ptr(),
+            v.data_ptr(), DTYPES[k.dtype], k.shape[0], cu_p, at_p, B, table_p, width)
+    return k, v
+
+
+def cache_attention_workspace_bytes(cache: KVCache, T: int, B: int, heads: int) -> int:
+    return int(_lib.oq_cache_attention_workspace_bytes(cache._ref, T, B, heads))
+
+
+def cache_attention(cache: KVCache, q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                    rpbh: Rpbh = None, scale: float = None, causal: bool = True, out=None, workspace=None,
+                    stream=None):
+    """Attention of the rows q (cuda bf16 / fp16 [T, heads, d], rows cu[b] ..
+    cu[b+1]-1 are sequence b's newest tokens) over the lens[b] tokens that the
+    sequence holds in the cache, these among them.  scale: 1/sqrt(d) if None."""
+    qt, qh = _rows("q", q, None, cache.d)
+    T, heads, d = q.shape
+    if q.device != cache.device:
+        raise ValueError(f"q must be on the cache's device {cache.device}")
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
+    ot, oh = _rows("out", out, heads, d, like=q)
+    cu_p, at_p, B, table_p, width = _batch(cache, cu, "lens", lens, table)
+    if workspace is None:
+        need = _lib.oq_cache_attention_workspace_bytes(cache._ref, T, B, heads)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on q's device")
+    _launch(_lib.oq_cache_attention, cache.device, stream, cache._ref, None if rpbh is None else rpbh.handle,
+            q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, DTYPES[q.dtype], heads, T, cu_p, at_p, B, table_p, width,
+            causal, d ** -0.5 if scale is None else scale, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out

@@ -53,7 +53,8 @@ extern "C" {
 
 enum {
   OQ_OK = 0,
-  OQ_ERR_ARG = 1,          /* null handle/pointer, bad size, mismatched handles */
+  OQ_ERR_ARG = 1,          /* null handle/pointer, bad size, mismatched handles; as a device
+                              status: an index in device memory was out of range */
   OQ_ERR_UNSUPPORTED = 2,  /* valid for the method but not for these kernels */
   OQ_ERR_ALIGN = 3,        /* a device pointer is not 16-byte aligned */
   OQ_ERR_CUDA = 4,         /* a CUDA runtime call failed (message has the name) */
@@ -79,7 +80,9 @@ OQ_API long long oq_device_allocations(void);
 OQ_API const char* oq_last_error(void);
 
 /* Reads and clears the device status word of the current device after
- * synchronising `stream`.  Returns OQ_OK, OQ_ERR_TIMEOUT, or OQ_ERR_CUDA. */
+ * synchronising `stream`.  Returns OQ_OK, OQ_ERR_TIMEOUT, OQ_ERR_ARG (a cache
+ * operator met a page, a length or a row offset out of range and left that part
+ * out), or OQ_ERR_CUDA. */
 OQ_API int oq_get_device_status(void* stream);
 
 /* Synchronous checking, for debugging: when on, every launching entry point
@@ -335,6 +338,132 @@ OQ_API int oq_linear(oq_rpbh_t r, oq_codebook_t cb_a, oq_codebook_t cb_w, const 
 OQ_API int oq_linear_noalloc(oq_rpbh_t r, oq_codebook_t cb_a, oq_codebook_t cb_w, const void* X, int M,
                              const uint8_t* w_codes, const void* w_norm, int N, const void* bias, int epilogue,
                              float* Y_f32, void* Y_bf16, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * What stands behind the fused QKV projection of a transformer block: rotary
+ * positions, a quantized cache of keys and values, attention over it.
+ * The OrbitQuant pages quantize the linear layers only; these operators carry
+ * the same rotation to the cache (a handle of the head's width), where it
+ * spreads the keys' loud channels so that one scale serves a whole page.
+ *
+ * Element types of the tensors below, and strides: a token's row of one head is
+ * contiguous; `*_token` and `*_head` are the strides, in elements, between
+ * tokens and between heads (slices of a fused [T][heads][d] tensor need no
+ * copy).  Base pointers are 16-byte aligned and strides multiples of 16 bytes
+ * (OQ_ERR_ALIGN), so that rows are too.
+ * ------------------------------------------------------------------------- */
+enum { OQ_BF16 = 0, OQ_FP16 = 1, OQ_FP32 = 2 };
+typedef struct oq_rope_s* oq_rope_t;
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions over several axes (time, height, width, ...)
+ *   (a, b) -> (a cos phi - b sin phi, a sin phi + b cos phi),
+ *   phi = pos[t][axis[p]] * freq[p]  for pair p of every head of token t.
+ * pairs  : 1..256; freq: host double[pairs], radians for each position, finite;
+ *          axis: host uint8[pairs], each below n_axes (1..8).
+ * layout : OQ_ROPE_INTERLEAVED  pair p is elements 2p and 2p + 1;
+ *          OQ_ROPE_HALVES       pair p is elements p and p + pairs.
+ * Elements from 2*pairs on are carried over bit for bit.
+ * The angle keeps its precision at any position: pos * freq is formed in turns
+ * as a 64-bit fixed-point product (error below |pos| * 2^-65 turns).
+ * Errors: OQ_ERR_ARG, OQ_ERR_NOMEM.
+ * ------------------------------------------------------------------------- */
+enum { OQ_ROPE_INTERLEAVED = 0, OQ_ROPE_HALVES = 1 };
+OQ_API int oq_make_rope(int pairs, const double* freq, const uint8_t* axis, int n_axes, int layout, oq_rope_t* out);
+/* Pairs, axes and layout of a handle.  Any output may be NULL. */
+OQ_API int oq_rope_info(oq_rope_t rope, int* pairs, int* n_axes, int* layout);
+OQ_API void oq_free_rope(oq_rope_t rope);
+
+/* Y = X turned.  X, Y: device [T][heads][d] of `dtype` (OQ_BF16, OQ_FP16,
+ * OQ_FP32); Y is X with the same strides (in place), or does not overlap it.
+ * pos: device int32 [T][n_axes], any values.  inverse != 0 turns by -phi: the
+ * inverse, and the gradient (dX from dY).
+ * d: 2*pairs <= d <= 512, d % 8 == 0 (OQ_ROPE_HALVES: pairs % 8 == 0 too;
+ * OQ_ERR_UNSUPPORTED).  T == 0 or heads == 0 launches nothing. */
+OQ_API int oq_rope_apply(oq_rope_t rope, const void* X, long long x_token, long long x_head, void* Y,
+                         long long y_token, long long y_head, int dtype, int T, int heads, int d, const int32_t* pos,
+                         int inverse, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The cache: pages of `page` tokens, each of one sequence, in 8-bit codes with
+ * a power-of-two scale for each page and head, keys and values apart:
+ *   value = code * scale,  code in -127..127,  scale = 2^e, -40 <= e <= 40.
+ * A sequence's tokens 0, 1, 2, ... lie in the pages table[b][0], table[b][1],
+ * ... (int32, one row of `width` entries for each sequence); entries behind its
+ * last page are not read.  A page may serve several sequences for reading
+ * (a shared prefix); one that is written to belongs to one sequence.
+ * heads >= 1, page in {16, 32, 64, 128}, d in {64, 128}; n_pages * page and
+ * width * page below 2^31 (OQ_ERR_UNSUPPORTED otherwise).  Pages need no
+ * preparation; a key scale of 0 marks a page as empty (attention skips it).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int8_t* k;      /* device [n_pages][heads][page][d], 16-byte aligned */
+  int8_t* v;
+  float* k_scale; /* device [n_pages][heads] */
+  float* v_scale;
+  int n_pages, heads, page, d;
+} oq_kvcache;
+
+/* Quantizes new keys and values as it writes them.
+ *   u = Pi x (r: a rotation of width d with one round and block >= 32, or NULL
+ *   for u = x);  code = round-to-nearest-even(u / 2^e)
+ * with e the least exponent that holds the page's new rows (max|u| <= 127 * 2^e,
+ * clamped to [-40, 40]; larger values saturate).  Where the page holds older
+ * tokens of the sequence, e is at least theirs, and when it grows by k their
+ * codes become round-to-nearest-even(code / 2^k): no value is ever off by more
+ * than one step of the scale that stands, however the tokens were portioned.
+ * Codes are decided in fp32: one may differ from the exact value's only where
+ * u / 2^e lies within 1e-3 of the border between two codes.
+ * K, V   : device [T][heads][d], OQ_BF16 or OQ_FP16, finite values (a NaN is
+ *          stored as 0, an infinity saturates).
+ * cu     : device int32 [B + 1], the new tokens of sequence b are rows cu[b] ..
+ *          cu[b+1] - 1; rows outside all sequences are not read.
+ * past   : device int32 [B], tokens that sequence b holds already (0: the page
+ *          is taken as new); the new ones follow.
+ * Two sequences must not write into one page.  A sequence whose numbers do not
+ * fit (cu out of 0..T or decreasing, past negative, more than width * page
+ * tokens) and a page outside 0..n_pages-1 are left out and reported in the
+ * device status (OQ_ERR_ARG).
+ * Errors: OQ_ERR_ARG (NULL, sizes, rotation of another width), OQ_ERR_ALIGN,
+ * OQ_ERR_UNSUPPORTED (cache geometry, dtype, composed rotation). */
+OQ_API int oq_cache_write(const oq_kvcache* cache, oq_rpbh_t r, const void* K, long long k_token, long long k_head,
+                          const void* V, long long v_token, long long v_head, int dtype, int T, const int32_t* cu,
+                          const int32_t* past, int B, const int32_t* table, int width, void* stream);
+
+/* Reads values back: row cu[b] + i is token first[b] + i of sequence b,
+ *   x = Pi^T (code * scale), rounded once to dtype.
+ * K, V   : device [T][heads][d] contiguous, OQ_BF16 or OQ_FP16.  Rows outside
+ *          all sequences, and rows whose place is out of range (reported in the
+ *          device status), are left as they were.
+ * Arguments and errors otherwise as oq_cache_write. */
+OQ_API int oq_cache_read(const oq_kvcache* cache, oq_rpbh_t r, void* K, void* V, int dtype, int T, const int32_t* cu,
+                         const int32_t* first, int B, const int32_t* table, int width, void* stream);
+
+/* Attention of new tokens over the cache:
+ *   O[i][h] = Pi^T sum_j p_j v_j,  p = softmax_j(scale * (Pi Q[i][h]) . k_j)
+ * with k, v the cache's rows of head h / (heads / cache->heads).
+ * Q, O   : device [T][heads][d], OQ_BF16 or OQ_FP16, heads a multiple of the
+ *          cache's (each of its heads serves that many query heads in a row);
+ *          O may not overlap Q.
+ * cu     : device int32 [B + 1], rows of sequence b, as above.
+ * lens   : device int32 [B], tokens of sequence b in the cache, the new ones
+ *          among them.
+ * causal : != 0: new token i of n sees the tokens 0 .. lens - n + i; else all
+ *          of them.  A row that sees none gives 0.
+ * scale  : of the scores (1/sqrt(d) as a rule), finite.
+ * workspace: device, 16-byte aligned, at least
+ *          oq_cache_attention_workspace_bytes(cache, T, B, heads); it keeps
+ *          nothing between calls, and calls that overlap need one each.
+ * Sums are fp32; queries and softmax weights go to the tensor cores in fp16
+ * beside powers of two of their own.  Rows outside all sequences, and those of
+ * a sequence whose numbers do not fit (device status), are left as they were;
+ * a page out of range counts as empty (device status).  The same call gives
+ * the same bits every time.  Errors as oq_cache_write. */
+OQ_API size_t oq_cache_attention_workspace_bytes(const oq_kvcache* cache, int T, int B, int heads);
+OQ_API int oq_cache_attention(const oq_kvcache* cache, oq_rpbh_t r, const void* Q, long long q_token, long long q_head,
+                              void* O, long long o_token, long long o_head, int dtype, int heads, int T,
+                              const int32_t* cu, const int32_t* lens, int B, const int32_t* table, int width,
+                              int causal, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,604 @@
+"""Rotary positions, the 8-bit cache and attention over it, on the GPU, against
+the fp64 oracle.
+
+Tolerances (eps = torch.finfo(dtype).eps, a rounding is off by eps / 2):
+  rope    an output is off by eps/2 of itself and by 6e-7 of its pair's length:
+          sincospif's 2 ulp of each (2^-23 sqrt 2 in all), the angle's float
+          (pi 2^-25) and three roundings of products and sums (3 * 2^-24).
+  codes   u / 2^e is computed with 7 additions and 2 products, so it is off by
+          9 * 2^-24 * sum|x| / sqrt h / 2^e <= 9 * 2^-24 * ||u|| / 2^e
+          <= 9 * 2^-24 * sqrt(128) * 127 < 8e-4 steps: a code may differ from
+          the oracle's, by one, only within 1e-3 of a border.
+  read    u = code * 2^e is exact; the transform's 7 additions and one product
+          are off by 8 * 2^-24 ||u|| at most, then eps/2 of the value.
+  attn    for each row, the oracle's bound (roundings of queries and weights to
+          fp16) plus eps/2 of the row's norm (+ 8 * 2^-24 of it for the turn).
+"""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oc
+from oracle import rpbh as orpbh
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def oq():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from calibration_free_rotated_b200 import build
+    build.build()
+    from calibration_free_rotated_b200 import orbitquant
+    return orbitquant
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def cum(v):
+    return [0] + list(np.cumsum(v))
+
+
+def rotation(oq, d, block, seed=0):
+    if not block:
+        return None, None
+    perm, signs = orpbh.draw_permutation_and_signs(seed, d)
+    return oq.Rpbh(seed, d, block), (perm, signs, block)
+
+
+def rows(rng, shape, dt, loud=True):
+    x = rng.standard_normal(shape)
+    if loud:
+        x = x * np.exp(0.4 * rng.standard_normal(shape[-2:])) * (1 + 7 * (rng.random(shape[-2:]) < 0.03))
+    return torch.from_numpy(x).to(DT[dt]).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------------ rope
+ROPES = [  # T, heads, d, axis_dims, layout, dtype
+    (1, 1, 64, (64,), "interleaved", "bf16"),
+    (1, 40, 128, (128,), "halves", "bf16"),
+    (17, 3, 128, (16, 56, 56), "interleaved", "fp16"),
+    (130, 24, 128, (44, 42, 42), "interleaved", "bf16"),
+    (33, 5, 128, (32, 32), "halves", "fp32"),          # a part of the head turns
+    (33, 5, 72, (30, 4), "interleaved", "bf16"),       # the turned part ends inside a vector
+    (33, 5, 72, (30, 4), "interleaved", "fp32"),
+    (9, 2, 40, (6,), "interleaved", "fp16"),
+    (5, 2, 24, (16,), "halves", "bf16"),               # one vector stands alone at the end
+    (7, 1, 512, (512,), "halves", "fp32"),
+    (7, 1, 512, (128, 128, 128, 128), "interleaved", "fp32"),
+    (3000, 2, 8, (4, 4), "interleaved", "fp32"),
+]
+
+
+@pytest.mark.parametrize("T,heads,d,dims,layout,dt", ROPES)
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope(oq, T, heads, d, dims, layout, dt, inverse):
+    rng = np.random.default_rng(T + d)
+    r = oq.Rope(dims, layout=layout)
+    fused = torch.from_numpy(rng.standard_normal((T, heads + 2, d))).to(DT[dt]).cuda()
+    x = fused[:, 1:1 + heads]
+    pos = rng.integers(-5, 2_000_000_000, (T, len(dims)))
+    pos[: T // 2] %= 70
+    freq = [10000.0 ** (-2 * k / n) for n in dims for k in range(n // 2)]
+    axis = [a for a, n in enumerate(dims) for _ in range(n // 2)]
+    want = oc.rope(f64(x), pos, freq, axis, layout == "halves", inverse)
+    got = f64(oq.rope_apply(r, x, ints(pos), inverse=inverse))
+    n = sum(dims) // 2
+    length = np.zeros(want.shape)
+    i = np.arange(n)
+    a, b = (i, i + n) if layout == "halves" else (2 * i, 2 * i + 1)
+    length[..., a] = length[..., b] = np.hypot(want[..., a], want[..., b])
+    # the angle's products in the oracle are rounded too: pos * freq to 2^-53 of itself
+    drift = np.zeros(want.shape)
+    phi = np.abs(pos[:, axis] * np.array(freq))[:, None] * 2.0 ** -51
+    drift[..., a] = drift[..., b] = phi
+    assert np.all(np.abs(got - want) <= torch.finfo(DT[dt]).eps / 2 * 1.001 * np.abs(want) + (6e-7 + drift) * length)
+    assert np.array_equal(got[..., 2 * n:], f64(x)[..., 2 * n:])  # carried over
+    keep = fused.clone()
+    oq.rope_apply(r, x, ints(pos), out=x, inverse=inverse)  # in place
+    assert np.array_equal(f64(x), got)
+    assert torch.equal(fused[:, 0], keep[:, 0]) and torch.equal(fused[:, 1 + heads:], keep[:, 1 + heads:])
+
+
+def test_rope_ladders_and_infinities(oq):
+    rng = np.random.default_rng(5)
+    x = rows(rng, (6, 2, 64), "fp32")
+    pos = rng.integers(0, 1000, (6, 3))
+    shared = [10000.0 ** (-2 * p / 48) for p in range(24)]
+    axis = [0] * 8 + [1] * 8 + [2] * 8
+    want = oc.rope(f64(x), pos, shared, axis, True)
+    got = oq.rope_apply(oq.Rope((16, 16, 16), layout="halves", ladder="shared"), x, ints(pos))
+    again = oq.rope_apply(oq.Rope(freqs=shared, axes=axis, layout="halves"), x, ints(pos))
+    assert torch.equal(got, again)
+    assert np.abs(f64(got) - want).max() <= 1e-6 * np.abs(want).max() * 2
+    # what is carried over keeps its bits, whatever stands in it
+    for dt in ("bf16", "fp32"):
+        y = rows(rng, (3, 1, 40), dt)
+        y[:, :, 6:] = float("inf")
+        y[1, 0, 7:20] = float("nan")
+        for layout, dims in (("interleaved", (6,)), ("halves", (16,))):
+            z = oq.rope_apply(oq.Rope(dims, layout=layout), y, ints(np.ones((3, 1))))
+            assert torch.equal(z.view(torch.int8)[..., sum(dims) * y.element_size():],
+                               y.view(torch.int8)[..., sum(dims) * y.element_size():])
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "halves"])
+def test_rope_gradient(oq, layout):
+    """dX = the inverse turn of dY: against a difference quotient of the forward
+    pass (linear, so exact up to rounding) and as the transpose."""
+    rng = np.random.default_rng(11)
+    r = oq.Rope((16, 24, 24), layout=layout)
+    pos = ints(rng.integers(0, 5000, (9, 3)))
+    x, dy, dx = (rows(rng, (9, 3, 64), "fp32", loud=False) for _ in range(3))
+    grad = oq.rope_apply(r, dy, pos, inverse=True)
+    up, down = oq.rope_apply(r, x + dx, pos), oq.rope_apply(r, x - dx, pos)
+    lhs = float(((up - down).double() / 2 * dy.double()).sum())
+    rhs = float((dx.double() * grad.double()).sum())
+    size = float(dx.double().norm() * dy.double().norm())
+    assert abs(lhs - rhs) <= 4e-6 * size
+    back = oq.rope_apply(r, oq.rope_apply(r, x, pos), pos, inverse=True)
+    assert float((back - x).abs().max()) <= 4e-6 * float(x.abs().max())
+
+
+# ----------------------------------------------------------------------- cache
+class Batch:
+    """Sequences with pages of their own in a shuffled pool."""
+
+    def __init__(self, rng, new, past, page, spare=2, extra_width=1):
+        self.new, self.past, self.page = new, past, page
+        self.total = [a + b for a, b in zip(new, past)]
+        self.width = max(max(-(-t // page) for t in self.total), 1) + extra_width
+        need = sum(-(-t // page) for t in self.total)
+        pool = list(rng.permutation(need + spare))
+        self.n_pages = need + spare
+        self.table = np.full((len(new), self.width), -7, dtype=np.int64)  # what is not needed is not read
+        for b, t in enumerate(self.total):
+            for s in range(-(-t // page)):
+                self.table[b, s] = pool.pop()
+        self.T = sum(new)
+        self.cu = cum(new)
+
+
+def snapshot(cache):
+    e = np.round(np.log2(np.maximum(f64(cache.k_scale), 2.0 ** -60))).astype(int)
+    ev = np.round(np.log2(np.maximum(f64(cache.v_scale), 2.0 ** -60))).astype(int)
+    return cache.k.cpu().numpy().astype(int), e, cache.v.cpu().numpy().astype(int), ev
+
+
+def check_write(oq, cache, bt, k, v, r, rot):
+    kc, ke, vc, ve = snapshot(cache)
+    oq.cache_write(cache, k, v, ints(bt.cu), ints(bt.past), ints(bt.table), rpbh=r)
+    oq.device_status()
+    gk, gke, gv, gve = snapshot(cache)
+    for codes, exps, got, gexp, x in ((kc, ke, gk, gke, k), (vc, ve, gv, gve, v)):
+        near = oc.write(codes, exps, f64(x), bt.cu, bt.past, bt.table, rot)
+        assert np.array_equal(exps, gexp)
+        diff = np.abs(got - codes)
+        assert diff.max() <= 1
+        free = np.zeros(codes.shape, bool)  # written, and near a border
+        P = bt.page
+        for b in range(len(bt.new)):
+            for i in range(bt.new[b]):
+                p = bt.past[b] + i
+                free[bt.table[b, p // P], :, p % P] = near[bt.cu[b] + i] < 1e-3
+        assert not np.any(diff.astype(bool) & ~free)
+        assert diff.sum() <= 0.002 * max(1000, near.size)
+
+
+WRITES = [  # new, past, heads, d, page, block, dtype
+    ([1], [0], 1, 64, 16, 64, "bf16"),
+    ([1, 1, 1], [0, 15, 16], 2, 128, 16, 128, "bf16"),
+    ([5, 0, 33, 1], [3, 9, 63, 127], 3, 128, 64, 64, "fp16"),
+    ([200], [0], 2, 64, 32, 32, "bf16"),
+    ([130, 7], [100, 0], 1, 128, 128, 128, "bf16"),
+    ([130, 7], [1, 60], 2, 64, 128, 0, "fp16"),
+    ([64, 16, 17], [0, 16, 47], 2, 64, 16, 0, "bf16"),
+]
+
+
+@pytest.mark.parametrize("new,past,heads,d,page,block,dt", WRITES)
+def test_write_and_read(oq, new, past, heads, d, page, block, dt):
+    rng = np.random.default_rng(sum(new) + d + page)
+    r, rot = rotation(oq, d, block)
+    bt = Batch(rng, new, past, page)
+    cache = oq.KVCache(bt.n_pages, heads, d, page)
+    cache.k.copy_(torch.from_numpy(rng.integers(-127, 128, cache.k.shape)))  # pages' last users
+    cache.v.copy_(torch.from_numpy(rng.integers(-127, 128, cache.k.shape)))
+    cache.k_scale.fill_(2.0 ** 9)
+    cache.v_scale.fill_(2.0 ** 9)
+    old = Batch.__new__(Batch)
+    old.__dict__.update(bt.__dict__)
+    old.new, old.past, old.T, old.cu = bt.past, [0] * len(new), sum(past), cum(bt.past)
+    if old.T:
+        check_write(oq, cache, old, rows(rng, (old.T, heads, d), dt), rows(rng, (old.T, heads, d), dt), r, rot)
+    # the new rows are larger: the pages' scales grow and the older codes are halved
+    fused = rows(rng, (bt.T + 2, 2 * heads + 1, d), dt)
+    fused *= 11
+    k, v = fused[:bt.T, 1:1 + heads], fused[:bt.T, 1 + heads:]
+    check_write(oq, cache, bt, k, v, r, rot)
+    # the same call again changes nothing
+    before = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    oq.cache_write(cache, k, v, ints(bt.cu), ints(bt.past), ints(bt.table), rpbh=r)
+    assert all(torch.equal(a, b) for a, b in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+
+    # read back: all of it, and a part from the middle, rows behind the last sequence left alone
+    for first, count in (([0] * len(new), bt.total), ([t // 3 for t in bt.total], [t - t // 3 for t in bt.total])):
+        cu = cum(count)
+        ko, vo = (torch.full((cu[-1] + 3, heads, d), 7.0, dtype=DT[dt], device="cuda") for _ in range(2))
+        oq.cache_read(cache, ints(cu), ints(first), ints(bt.table), rpbh=r, k=ko, v=vo)
+        oq.device_status()
+        for codes, scale, got in ((cache.k, cache.k_scale, ko), (cache.v, cache.v_scale, vo)):
+            assert torch.all(got[cu[-1]:] == 7.0)
+            for b in range(len(new)):
+                u = oc.gather(codes.cpu().numpy(), f64(scale), bt.table[b], bt.total[b])[first[b]:]
+                x = oc.turn_back(u, rot)
+                tol = torch.finfo(DT[dt]).eps / 2 * 1.001 * np.abs(x) + 8 * 2.0 ** -24 * np.linalg.norm(u, axis=-1)[..., None]
+                if rot is None and dt == "bf16":
+                    tol = 0 * x  # 7 bits times a power of two: exact
+                assert np.all(np.abs(f64(got[cu[b]:cu[b + 1]]) - x) <= tol)
+
+
+def test_portions_stay_within_a_step(oq):
+    """Tokens written one by one, each louder than the last, against the values
+    themselves: no more than one step of the scale that stands."""
+    rng = np.random.default_rng(3)
+    d, heads, page = 64, 2, 16
+    r, rot = rotation(oq, d, 64)
+    cache = oq.KVCache(2, heads, d, page)
+    x = rows(rng, (16, heads, d), "bf16", loud=False)
+    x *= (1.3 ** torch.arange(16, device="cuda"))[:, None, None].to(x.dtype)
+    table = ints([[1]])
+    for t in range(16):
+        oq.cache_write(cache, x[t:t + 1], x[t:t + 1], ints([0, 1]), ints([t]), table, rpbh=r)
+    u = oc.turn(f64(x), rot)
+    got = oc.gather(cache.k.cpu().numpy(), f64(cache.k_scale), [1], 16)
+    step = f64(cache.k_scale)[1][None, :, None]
+    assert np.all(np.abs(got - u) <= step * 1.001)
+    assert np.abs(got - u).max() > 0.5 * step.min()  # the halvings did happen
+
+
+def test_write_extremes(oq):
+    d = 64
+    cache = oq.KVCache(6, 1, d, 16)
+    x = torch.zeros((6, 1, d), dtype=torch.bfloat16, device="cuda")
+    x[1] = 3e38          # saturates
+    x[2, 0, 0] = float("inf")
+    x[3, 0, 0] = float("nan")
+    x[3, 0, 1] = 127.0
+    x[4] = 2.0 ** -60    # below the smallest step
+    x[5, 0, :3] = torch.tensor([127.0, 0.5, 1.5])  # the largest value of a scale; ties go to even
+    oq.cache_write(cache, x, x, ints(range(7)), ints([0] * 6), ints([[b] for b in range(6)]))
+    oq.device_status()
+    k, s = cache.k[:, 0, 0].cpu().numpy(), f64(cache.k_scale)[:, 0]
+    assert not k[0].any() and s[0] == 2.0 ** -40
+    assert np.all(k[1] == 127) and s[1] == 2.0 ** 40
+    assert k[2, 0] == 127 and not k[2, 1:].any()
+    assert k[3, 0] == 0 and k[3, 1] == 127 and s[3] == 1.0
+    assert not k[4].any() and s[4] == 2.0 ** -40
+    assert list(k[5, :3]) == [127, 0, 2] and s[5] == 1.0
+    ko, _ = oq.cache_read(cache, ints(range(7)), ints([0] * 6), ints([[b] for b in range(6)]), T=6)
+    assert torch.isfinite(ko.float()).all()
+
+
+def test_bad_indices_are_left_out(oq):
+    """Pages and lengths out of range: the others are served, the status says so."""
+    rng = np.random.default_rng(8)
+    d, heads, P = 64, 2, 16
+    cache = oq.KVCache(4, heads, d, P)
+    k = rows(rng, (8, heads, d), "bf16")
+    cu = ints([0, 2, 4, 6, 8])
+    good = ([[0, 1], [4, 1], [-1, 0], [2, 3]], [0, 0, 0, 15])
+    for table, past in (good, ([[0, 1], [1, 1], [2, 0], [3, 3]], [0, -3, 31, 2 ** 31 - 1])):
+        cache.k.zero_()
+        oq.cache_write(cache, k, k, cu, ints(past), ints(table))
+        with pytest.raises(oq.OQError) as e:
+            oq.device_status()
+        assert e.value.code == oq.OQ_ERR_ARG
+        oq.device_status()  # cleared
+        assert cache.k[0, :, :2].any() and not cache.k[0, :, 2:].any()
+        out = torch.full((8, heads, d), 5.0, dtype=torch.bfloat16, device="cuda")
+        vo = out.clone()
+        oq.cache_read(cache, cu, ints(past), ints(table), k=out, v=vo)
+        with pytest.raises(oq.OQError):
+            oq.device_status()
+        assert torch.all(out[2:4] == 5.0)
+    assert not cache.k[1].any()  # only the bad sequences have it
+    # decreasing and overlong offsets
+    for bad in ([0, 2, 1, 3, 9], [-1, 2, 4, 6, 8], [2, 0, 0, 0, 100]):
+        oq.cache_write(cache, k, k, ints(bad), ints([0] * 4), ints([[0], [1], [2], [3]]))
+        with pytest.raises(oq.OQError):
+            oq.device_status()
+    # attention: a page out of range counts as empty, a sequence that does not fit is left alone
+    cache = oq.KVCache(4, heads, d, P)
+    oq.cache_write(cache, k, k, ints([0, 8]), ints([0]), ints([[2]]))
+    q = rows(rng, (2, heads, d), "bf16")
+    one = oq.cache_attention(cache, q[:1], ints([0, 1]), ints([8]), ints([[2]]))
+    oq.device_status()
+    out = torch.full((2, heads, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    oq.cache_attention(cache, q, ints([0, 1, 2]), ints([24, 99]), ints([[2, 9], [2, 2]]), out=out)
+    with pytest.raises(oq.OQError):
+        oq.device_status()
+    assert torch.all(out[1] == 5.0)
+    two = oq.cache_attention(cache, q[:1], ints([0, 1]), ints([16]), ints([[2]]))
+    oq.device_status()
+    assert torch.equal(out[:1], two) and one.shape == two.shape
+
+
+# ------------------------------------------------------------------- attention
+def filled(oq, rng, bt, heads, d, r, dt="bf16", loud=True):
+    cache = oq.KVCache(bt.n_pages, heads, d, bt.page)
+    n = sum(bt.total)
+    if n:
+        oq.cache_write(cache, rows(rng, (n, heads, d), dt, loud), rows(rng, (n, heads, d), dt, loud),
+                       ints(cum(bt.total)), ints([0] * len(bt.total)), ints(bt.table), rpbh=r)
+    return cache
+
+
+def check_attention(oq, cache, bt, q, r, rot, causal, scale=None, empty_page=None):
+    n_rows = q.shape[0]
+    out = torch.full((n_rows, q.shape[1], q.shape[2]), 9.0, dtype=q.dtype, device="cuda")
+    oq.cache_attention(cache, q, ints(bt.cu), ints(bt.total), ints(bt.table), rpbh=r, causal=causal, scale=scale, out=out)
+    oq.device_status()
+    assert torch.all(out[bt.cu[-1]:] == 9.0)
+    eps = torch.finfo(q.dtype).eps
+    codes = [c.cpu().numpy() for c in (cache.k, cache.v)]
+    scales = [f64(s) for s in (cache.k_scale, cache.v_scale)]
+    for b in range(len(bt.new)):
+        k, v = (oc.gather(c, s, bt.table[b], bt.total[b]) for c, s in zip(codes, scales))
+        empty = None
+        if empty_page is not None:
+            empty = np.array([[scales[0][bt.table[b][t // bt.page], h] == 0 for h in range(cache.heads)]
+                              for t in range(bt.total[b])]).reshape(bt.total[b], cache.heads)
+        want, bound = oc.attention(f64(q[bt.cu[b]:bt.cu[b + 1]]), k, v, causal,
+                                   q.shape[2] ** -0.5 if scale is None else scale, rot, empty)
+        got = f64(out[bt.cu[b]:bt.cu[b + 1]])
+        err = np.linalg.norm(got - want, axis=-1)
+        limit = bound + (eps / 2 + 8 * 2.0 ** -24) * 1.01 * np.linalg.norm(want, axis=-1)
+        assert np.all(err <= limit), (b, (err / np.maximum(limit, 1e-300)).max())
+    return out
+
+
+ATTN = [  # new, past, heads, group, d, page, block, dtype, causal
+    ([1], [0], 1, 1, 64, 16, 64, "bf16", True),
+    ([1], [16], 2, 4, 128, 16, 128, "bf16", True),
+    ([1, 1, 1, 1], [517, 0, 63, 64], 2, 8, 128, 64, 128, "bf16", True),
+    ([1] * 7, [3, 900, 31, 32, 33, 2000, 1], 3, 5, 64, 32, 32, "fp16", True),
+    ([1, 1], [1300, 700], 1, 16, 128, 128, 0, "bf16", True),
+    ([1], [5000], 1, 1, 128, 64, 128, "bf16", False),
+    ([4, 0, 2, 7], [100, 10, 1, 0], 2, 2, 64, 16, 64, "bf16", True),
+    ([5, 3], [64, 200], 1, 3, 128, 32, 64, "fp16", False),
+    ([37, 1, 90], [0, 300, 45], 2, 2, 64, 64, 64, "fp16", True),
+    ([129, 40], [70, 0], 2, 1, 128, 16, 128, "bf16", True),
+    ([129, 40], [70, 11], 1, 4, 128, 64, 0, "bf16", False),
+    ([300], [0], 1, 2, 64, 128, 64, "bf16", True),
+]
+
+
+@pytest.mark.parametrize("new,past,heads,group,d,page,block,dt,causal", ATTN)
+def test_attention(oq, new, past, heads, group, d, page, block, dt, causal):
+    rng = np.random.default_rng(sum(new) + sum(past) + d)
+    r, rot = rotation(oq, d, block)
+    bt = Batch(rng, new, past, page)
+    cache = filled(oq, rng, bt, heads, d, r, dt)
+    fused = rows(rng, (bt.T + 3, heads * group + 2, d), dt, loud=False) * 2
+    check_attention(oq, cache, bt, fused[:, 1:1 + heads * group], r, rot, causal)
+
+
+def test_attention_scales_far_apart(oq):
+    """Pages whose values differ by many powers of two, and the score's own range."""
+    rng = np.random.default_rng(21)
+    r, rot = rotation(oq, 64, 64)
+    bt = Batch(rng, [1, 2], [200, 90], 16)
+    cache = filled(oq, rng, bt, 1, 64, r)
+    cache.v_scale *= torch.exp2(torch.from_numpy(rng.integers(-12, 13, (bt.n_pages, 1))).cuda()).float()
+    cache.k_scale *= torch.exp2(torch.from_numpy(rng.integers(-3, 2, (bt.n_pages, 1))).cuda()).float()
+    for scale in (None, 0.0, -0.3, 2.0):
+        check_attention(oq, cache, bt, rows(rng, (3, 2, 64), "fp16", loud=False), r, rot, True, scale)
+    q = rows(rng, (3, 2, 64), "bf16", loud=False)
+    for f in (1e-30, 1e25):  # a query's own power of two
+        check_attention(oq, cache, bt, q * f, r, rot, True, 0.1 / f)
+
+
+def test_attention_rows_without_keys(oq):
+    rng = np.random.default_rng(22)
+    bt = Batch(rng, [5, 3, 2], [0, 0, 4], 16)
+    bt.total = [2, 0, 6]  # fewer tokens than queries; none at all
+    cache = filled(oq, rng, bt, 2, 64, None)
+    q = rows(rng, (10, 4, 64), "bf16")
+    out = check_attention(oq, cache, bt, q, None, None, True)
+    assert not out[:3].any() and out[3:5].any() and not out[5:8].any()
+    out = check_attention(oq, cache, bt, q, None, None, False)
+    assert out[:5].any() and not out[5:8].any()
+    # pages that hold nothing (a key scale of 0)
+    bt = Batch(rng, [1, 1], [100, 20], 16)
+    cache = filled(oq, rng, bt, 2, 64, None)
+    cache.k_scale[bt.table[0, 2]] = 0
+    cache.k_scale[bt.table[1, :2]] = 0
+    out = check_attention(oq, cache, bt, q[:2], None, None, True, empty_page=True)
+    assert out[0].any() and not out[1].any()
+
+
+def test_attention_nan_query_stays_in_its_row(oq):
+    rng = np.random.default_rng(23)
+    r, rot = rotation(oq, 128, 128)
+    bt = Batch(rng, [3], [700], 64)
+    cache = filled(oq, rng, bt, 1, 128, r)
+    q = rows(rng, (3, 2, 128), "bf16")
+    clean = oq.cache_attention(cache, q, ints(bt.cu), ints(bt.total), ints(bt.table), rpbh=r)
+    q[1, 1, 5] = float("nan")
+    out = oq.cache_attention(cache, q, ints(bt.cu), ints(bt.total), ints(bt.table), rpbh=r)
+    assert torch.isnan(out[1, 1]).all()
+    out[1, 1] = clean[1, 1]
+    assert torch.equal(out, clean)
+
+
+def test_attention_ignores_what_it_may_not_see(oq):
+    """Codes behind the last token, other pages and their scales change nothing."""
+    rng = np.random.default_rng(24)
+    r, rot = rotation(oq, 64, 64)
+    bt = Batch(rng, [1, 6], [21, 77], 32)
+    cache = filled(oq, rng, bt, 2, 64, r)
+    q = rows(rng, (7, 4, 64), "bf16")
+    args = (ints(bt.cu), ints(bt.total), ints(bt.table))
+    clean = oq.cache_attention(cache, q, *args, rpbh=r)
+    used = {int(bt.table[b, s]) for b in range(2) for s in range(-(-bt.total[b] // 32))}
+    for p in range(bt.n_pages):
+        if p not in used:
+            cache.k[p], cache.v[p] = -127, 127
+            cache.k_scale[p], cache.v_scale[p] = float("nan"), float("inf")
+    cache.k[bt.table[0, 0], :, 22:], cache.v[bt.table[0, 0], :, 22:] = 127, -128
+    cache.v[bt.table[1, 2], :, 83 - 64:] = -128
+    assert torch.equal(clean, oq.cache_attention(cache, q, *args, rpbh=r))
+
+
+def test_shared_pages_and_a_batch_beyond_one_block(oq):
+    """Many sequences over one shared prefix; the sequences outnumber a CTA's threads."""
+    rng = np.random.default_rng(25)
+    r, rot = rotation(oq, 64, 64)
+    B, P = 300, 16
+    lens = [int(n) for n in rng.integers(0, 65, B)]
+    cache = oq.KVCache(4, 1, 64, P)
+    x = rows(rng, (64, 1, 64), "bf16")
+    oq.cache_write(cache, x, x, ints([0, 64]), ints([0]), ints([[2, 0, 3, 1]]), rpbh=r)
+    q = rows(rng, (B, 2, 64), "bf16")
+    table = ints([[2, 0, 3, 1]] * B)
+    out = oq.cache_attention(cache, q, ints(range(B + 1)), ints(lens), table, rpbh=r)
+    k = oc.gather(cache.k.cpu().numpy(), f64(cache.k_scale), [2, 0, 3, 1], 64)
+    v = oc.gather(cache.v.cpu().numpy(), f64(cache.v_scale), [2, 0, 3, 1], 64)
+    for b in range(0, B, 13):
+        want, bound = oc.attention(f64(q[b:b + 1]), k[:lens[b]], v[:lens[b]], False, 0.125, rot)
+        err = np.linalg.norm(f64(out[b:b + 1]) - want, axis=-1)
+        assert np.all(err <= bound + (2.0 ** -8 + 2.0 ** -20) * np.linalg.norm(want, axis=-1))
+    # writing and reading with as many sequences
+    cache = oq.KVCache(B, 1, 64, P)
+    new = [int(n) for n in rng.integers(0, 5, B)]
+    y = rows(rng, (sum(new), 1, 64), "bf16")
+    tb = ints(rng.permutation(B)[:, None])
+    oq.cache_write(cache, y, y, ints(cum(new)), ints([0] * B), tb, rpbh=r)
+    ko, vo = oq.cache_read(cache, ints(cum(new)), ints([0] * B), tb, T=sum(new), rpbh=r)
+    oq.device_status()
+    assert torch.equal(ko, vo)
+    assert float((ko.double() - y.double()).norm() / y.double().norm()) < 0.03
+
+
+# ----------------------------------------------------------- streams, graphs, devices
+def test_streams_and_graphs(oq):
+    """The operators on a stream of their own and in two captured graphs that share a workspace."""
+    rng = np.random.default_rng(31)
+    r, _ = rotation(oq, 128, 128)
+    rope = oq.Rope((16, 56, 56))
+    bt = Batch(rng, [1, 3], [300, 40], 64)
+    q, k, v = (rows(rng, (4, n, 128), "bf16") for n in (8, 2, 2))
+    pos = ints(rng.integers(0, 100, (4, 3)))
+    cu, past, total, table = ints(bt.cu), ints(bt.past), ints(bt.total), ints(bt.table)
+    ws = torch.empty((oq.cache_attention_workspace_bytes(oq.KVCache(1, 2, 128), 4, 2, 8),), dtype=torch.uint8,
+                     device="cuda")
+    base = filled(oq, rng, bt, 2, 128, r)
+
+    def step(cache, out, stream=None):
+        oq.cache_write(cache, oq.rope_apply(rope, k, pos, stream=stream), v, cu, past, table, rpbh=r, stream=stream)
+        oq.cache_attention(cache, oq.rope_apply(rope, q, pos, stream=stream), cu, total, table, rpbh=r, out=out,
+                           workspace=ws, stream=stream)
+
+    def fresh():
+        return oq.KVCache.wrap(*(t.clone() for t in (base.k, base.v, base.k_scale, base.v_scale)))
+
+    want, cache = torch.empty_like(q), fresh()
+    step(cache, want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, other = torch.empty_like(q), fresh()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step(other, got)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(cache.k, other.k)
+    got.zero_()
+    third = fresh()
+    torch.cuda.synchronize()
+    kr, qr = oq.rope_apply(rope, k, pos), oq.rope_apply(rope, q, pos)
+    torch.cuda.synchronize()
+    oq.cache_write(third, kr, v, cu, past, table, rpbh=r, stream=side)
+    oq.cache_attention(third, qr, cu, total, table, rpbh=r, out=got, workspace=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    caches, outs, graphs = [fresh(), fresh()], [torch.zeros_like(q) for _ in range(2)], []
+    for c, o in zip(caches, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(c, o)
+        graphs.append(g)
+    for g in (graphs[0], graphs[1], graphs[0]):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+    oq.device_status()
+
+
+def test_no_library_allocations(oq):
+    rng = np.random.default_rng(32)
+    r, _ = rotation(oq, 64, 64)
+    rope = oq.Rope((64,))
+    bt = Batch(rng, [2], [9], 16)
+    cache = filled(oq, rng, bt, 1, 64, r)
+    x = rows(rng, (2, 1, 64), "bf16")
+    n = oq.device_allocations()
+    oq.cache_write(cache, oq.rope_apply(rope, x, ints([[1], [2]])), x, ints(bt.cu), ints(bt.past), ints(bt.table), rpbh=r)
+    oq.cache_attention(cache, x, ints(bt.cu), ints(bt.total), ints(bt.table), rpbh=r)
+    oq.cache_read(cache, ints(bt.cu), ints([0]), ints(bt.table), T=2, rpbh=r)
+    assert oq.device_allocations() == n
+
+
+def test_a_block_from_its_projection_on(oq):
+    """The operators together as a transformer block uses them, two steps of a
+    stream: fused QKV by the codebook linear, rotary positions in place on the
+    queries and keys, cache write, attention, output projection.  Held to fp64
+    attention on what the cache holds, and to attention on the unquantized
+    keys and values within the 8-bit cache's own loss."""
+    rng = np.random.default_rng(33)
+    d_model, H, d = 256, 4, 64
+    rm, rh = oq.Rpbh(0, d_model, 64), oq.Rpbh(3, d, 64)
+    perm, signs = orpbh.draw_permutation_and_signs(3, d)
+    cb = oq.Codebook(d_model, 4)
+    w = [oq.quantize_weight(rm, cb, (0.06 * torch.randn(n, d_model, device="cuda")).bfloat16()) for n in (3 * d_model, d_model)]
+    rope = oq.Rope((16, 24, 24))
+    cache = oq.KVCache(5, H, d, 16)
+    table = ints([[4, 2, 0], [1, 3, 3]])
+    seen_k, seen_v = [np.zeros((0, H, d))] * 2, [np.zeros((0, H, d))] * 2
+    for new, past in (([20, 11], [0, 0]), ([1, 4], [20, 11])):
+        T, cu = sum(new), cum(new)
+        x = torch.randn(T, d_model, device="cuda").bfloat16()
+        pos = ints([[b, i, i % 7] for b, n in enumerate(new) for i in range(n)])
+        _, qkv = oq.linear(rm, cb, cb, x, *w[0], want_f32=False, want_bf16=True)
+        qkv = qkv.view(T, 3 * H, d)
+        oq.rope_apply(rope, qkv[:, :2 * H], pos, out=qkv[:, :2 * H])
+        q, k, v = qkv[:, :H], qkv[:, H:2 * H], qkv[:, 2 * H:]
+        oq.cache_write(cache, k, v, ints(cu), ints(past), table, rpbh=rh)
+        total = [a + b for a, b in zip(new, past)]
+        o = oq.cache_attention(cache, q, ints(cu), ints(total), table, rpbh=rh)
+        y, _ = oq.linear(rm, cb, cb, o.view(T, d_model), *w[1])
+        oq.device_status()
+        assert y.shape == (T, d_model) and torch.isfinite(y).all()
+        for b in range(2):
+            sl = slice(cu[b], cu[b + 1])
+            seen_k[b] = np.concatenate([seen_k[b], f64(k[sl])])
+            seen_v[b] = np.concatenate([seen_v[b], f64(v[sl])])
+            kq, vq = (oc.gather(c.cpu().numpy(), f64(s), table[b].tolist(), total[b])
+                      for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+            want, bound = oc.attention(f64(q[sl]), kq, vq, True, d ** -0.5, (perm, signs, 64))
+            err = np.linalg.norm(f64(o[sl]) - want, axis=-1)
+            assert np.all(err <= bound + (2.0 ** -8 + 2.0 ** -20) * np.linalg.norm(want, axis=-1))
+            full, _ = oc.attention(f64(q[sl]), seen_k[b], seen_v[b], True, d ** -0.5, None)
+            assert np.linalg.norm(f64(o[sl]) - full) <= 0.05 * np.linalg.norm(full)

@@ -411,8 +411,6 @@ step_kernel(const __grid_constant__ Args a) {
   if (threadIdx.x == 0) a.desc[cta] = desc;
 }
 
-constexpr int kMaxCtas = 148 * 4;
-
 struct Plan {
   int rows;  // of a tile
   int ctas;  // most
@@ -420,8 +418,8 @@ struct Plan {
 Plan plan_of(int T, int B, int group) {
   Plan p;
   const long long per = ((long long)T * group + B - 1) / std::max(1, B);  // rows of a sequence, on average
-  p.rows = per <= 8 ? 8 : 16;
-  p.ctas = kMaxCtas;
+  p.rows = per <= 8 ? 8 : per <= 16 ? 16 : 128;
+  p.ctas = p.rows == 128 ? kChunkCtas : kStepCtas;
   return p;
 }
 
@@ -476,6 +474,7 @@ int launch_cattn(const AttnCall& c) {
   a.piece = static_cast<float*>(c.workspace);
   a.stat = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d));
   a.desc = reinterpret_cast<int4*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d) + stat_bytes(p));
+  if (p.rows == 128) return launch_cattn_chunk(a, c.dtype, v->d, c.stream);
   cudaStream_t s = (cudaStream_t)c.stream;
 #define OQ_STEP(T, D) return p.rows == 8 ? launch_step<T, D, 1>(a, p.ctas, s) : launch_step<T, D, 2>(a, p.ctas, s)
   if (c.dtype == OQ_BF16) {

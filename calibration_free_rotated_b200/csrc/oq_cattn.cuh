@@ -25,6 +25,8 @@ namespace cattn {
 using namespace cache;
 
 constexpr int kTile = 64;  // keys of a tile: the unit of work
+// Most CTAs that the workspace has pieces for (the kernels' residency on 148 SMs).
+constexpr int kStepCtas = 148 * 4, kChunkCtas = 148 * 2;
 
 struct Args {
   View c;
@@ -229,4 +231,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 }  // namespace cattn
+
+int launch_cattn_chunk(const cattn::Args& a, int dtype, int d, void* stream);  // oq_cattn_tc.cu
+
 }  // namespace oq

@@ -1,0 +1,645 @@
+// Attention over the 8-bit cache for many query rows (chunks of new tokens,
+// whole images): bound by the tensor cores and what feeds them.
+//
+// The same sums as oq_cattn.cu, on tcgen05: a CTA takes 128 query rows and walks
+// 64 keys a step.  Two roles of four warps:
+//   warps 4..7  expand the step's codes to fp16 (exact) into the K-major
+//               128-byte-swizzled layout of the tensor cores' operands, the keys
+//               as they lie, the values transposed by byte permutes; two stages
+//               each, the codes of the next step already in registers.
+//   warps 0..3  one thread a row: scores from TMEM, running maximum and sum,
+//               weights back into TMEM.  Warp 0 also issues the products: it
+//               would wait for them anyway.
+// TMEM, 256 columns, so that two CTAs share an SM and one's products run beside
+// the other's exponentials: the turned query (fp16, the left operand of the
+// scores), 64 columns of scores, whose first half the weights take over (the
+// left operand of the sum), and the sum itself, which stays until the end.
+//
+// Scales: as in oq_cattn.cu the running maximum is taken over score + ev, so
+// the weights carry their page's value exponent; a step's four groups of 16
+// tokens (no page is smaller) have their own.  The accumulator is rescaled only
+// when a row's maximum has grown by more than 2^8.
+//
+// fp16 queries keep a second term: the turn rounds them to 2^-12, which would
+// show beside an fp16 result, so what the first operand leaves out goes into a
+// second one (shared memory) and the scores take both.
+//
+// Every wait is bounded (~1 s); one that gives up records OQ_ERR_TIMEOUT and
+// raises a flag that lets all others return at once, and the CTA still reaches
+// its end and frees its TMEM.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "oq_cattn.cuh"
+
+namespace oq {
+namespace {
+
+using namespace cattn;
+
+constexpr int kThreads = 256, kRows = 128;
+constexpr int kTmem = 256, kColQ = 0, kColS = 64, kColO = 128;
+constexpr unsigned long long kWaitLimitNs = 1000000000ull;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ unsigned long long global_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  const unsigned long long t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        atomicExch(status, OQ_ERR_TIMEOUT);
+        *abort_flag = 1;
+        return;
+      }
+    }
+  }
+}
+__device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Operand descriptor: K-major, 128-byte swizzle, groups of eight rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// Instruction descriptor: D f32, A and B f16, both K-major, M = 128.
+template <int N>
+__host__ __device__ constexpr uint32_t idesc() {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+template <int N>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc<N>()), "r"(accumulate)
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b) {  // accumulates
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, 1, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc<N>())
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(t));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(t));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+template <int D, bool TWO>
+struct Smem {
+  static constexpr int kK = 2 * D * kTile;  // bytes of a stage of keys, and of values
+  static constexpr int kKeys = 0, kValues = 2 * kK;
+  static constexpr int kLow = 4 * kK;       // the query's second term
+  static constexpr int kRowStage = kLow + (TWO ? kRows * D * 2 : 0);      // 16-bit rows being turned
+  static constexpr int kScales = kRowStage + kThreads / (D / 8) * D * 2;  // [4][4] (key scale, ev, 2^-ev)
+  static constexpr int kFac = kScales + 4 * 4 * 16;                       // [rows] factor, limit
+  static constexpr int kStat = kFac + kRows * 8;                          // [rows] maximum, sum
+  static constexpr int kBars = kStat + kRows * 8;
+  static constexpr int kTotal = kBars + 128;
+  static constexpr int kAlloc = kTotal + 1024;  // room to align the base
+  // aliases of the stages, outside the steps
+  static constexpr int kQStride = D + 8;  // the query rows as fp16, before they go to TMEM
+  static_assert(kRows * kQStride * 2 <= kLow && kRows * D * 4 <= kLow, "what stands in the stages' place");
+  static_assert(2 * (kAlloc + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+
+template <typename T, int D, bool TWO>
+__global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constant__ Args a) {
+  using S = Smem<D, TWO>;
+  constexpr int LPR = D / 8;
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t base = smem_u32(sm);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float* row_fac = reinterpret_cast<float*>(sm + S::kFac);
+  int* row_lim = reinterpret_cast<int*>(sm + S::kFac) + kRows;
+  float2* row_stat = reinterpret_cast<float2*>(sm + S::kStat);
+  float4* scales = reinterpret_cast<float4*>(sm + S::kScales);
+  __half* qs = reinterpret_cast<__half*>(sm);
+  const uint32_t bars = base + S::kBars;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + S::kBars + 104);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 112);
+  auto bar = [&](int i) { return bars + 8u * i; };
+  constexpr int K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 9, O_FULL = 10;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(K_FULL + i), 4), mbar_init(bar(K_EMPTY + i), 1);
+      mbar_init(bar(V_FULL + i), 4), mbar_init(bar(V_EMPTY + i), 1);
+    }
+    mbar_init(bar(S_FULL), 1), mbar_init(bar(P_FULL), 4), mbar_init(bar(O_FULL), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                 "r"(kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  const int cta = blockIdx.x;
+  const Share sh = find_share<kRows, kThreads>(a, cta, gridDim.x);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
+
+  long long at = sh.size * cta;
+  const long long stop = min(sh.total, at + sh.size);
+  int4 desc = make_int4(0, 0, 0, 0);
+  int b = sh.b;
+  long long into = sh.into;
+  uint32_t steps = 0, items = 0;  // so far: the barriers' phases
+  const int l = tid % LPR;
+  const LaneTurn turn = lane_turn(a.r, l);
+  T* stage_row = reinterpret_cast<T*>(sm + S::kRowStage) + (tid / LPR) * D;
+  const int plog = 31 - __clz(a.c.page);
+
+  while (at < stop && b < a.B) {
+    const Seq s = load_seq(a, b, false);
+    const long long per_head = head_work<kRows>(a, s);
+    if (into >= per_head * a.c.heads) {
+      ++b;
+      into = 0;
+      continue;
+    }
+    const int h = (int)(into / per_head);
+    long long rem = into - h * per_head;
+    int qt = 0, work = tile_work<kRows>(a, s, 0);
+    while (rem >= work) {
+      rem -= work;
+      work = tile_work<kRows>(a, s, ++qt);
+    }
+    const int t0 = (int)rem, take = (int)min((long long)(work - t0), stop - at);
+    const int keys = tile_keys<kRows>(a, s, qt);
+    const int rows = min(kRows, s.rows - qt * kRows);
+
+    // the item's query rows: turned, scaled by a power of two, fp16
+    constexpr int PASS = kThreads / LPR, BATCH = 4;
+    for (int p = 0; p < kRows; p += BATCH * PASS) {
+      uint4 w[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int r = p + k * PASS + tid / LPR, gr = qt * kRows + r, i = gr / a.group;
+        w[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows)
+          w[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + i) * a.qt +
+                                                 ((long long)h * a.group + (gr - i * a.group)) * a.qh + 8 * l);
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int r = p + k * PASS + tid / LPR, i = (qt * kRows + r) / a.group;
+        float x[8];
+        if (a.r.perm) {
+          *reinterpret_cast<uint4*>(stage_row + 8 * l) = w[k];
+          __syncwarp();
+          rotate_row<T>(stage_row, turn, l, a.r, x);
+          __syncwarp();
+        } else {
+          unpack8<T>(w[k], x);
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+        for (int m = LPR / 2; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+        const int e = min(max(scale_exp(top), -100), 120);
+        const float f = pow2(-e);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= f;
+        const uint4 hi = pack8<__half>(x);
+        *reinterpret_cast<uint4*>(qs + r * S::kQStride + 8 * l) = hi;
+        if constexpr (TWO) {
+          float y[8];
+          unpack8<__half>(hi, y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = x[j] - y[j];
+          const uint4 lo = pack8<__half>(y);
+          sts128(base + S::kLow + (l >> 3) * (kRows * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
+        }
+        if (l == 0) {
+          row_fac[r] = pow2(e) * a.scale;
+          row_lim[r] = r >= rows ? 0x7FFFFFFF : a.causal ? s.len - s.n + i + 1 : s.len;  // no row: not masked, not used
+        }
+      }
+    }
+    if constexpr (TWO) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (warp < 4) {
+      const uint4* q = reinterpret_cast<const uint4*>(qs + tid * S::kQStride);
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 w = q[8 * c + j];
+          v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
+        }
+        tmem_st32(tmem_row + kColQ + 32 * c, v);
+      }
+      wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();  // the query stands in TMEM, its staging may be written over
+    tc_fence_after();
+
+    const int tok0 = t0 * kTile;
+    if (warp >= 4) {
+      // ---- expanding the codes ----
+      const int ct = tid - 128;
+      const int kn = ct & 63, kh = ct >> 6;           // a token's row, which half of it
+      const int vc = ct & 7, vg = ct >> 3;            // eight tokens, D / 16 coordinates
+      constexpr int KW = D / 32;                      // 16-byte vectors of codes of half a row
+      constexpr int VW = D / 64;                      // words of D / 16 codes
+      const int* table = a.table + (size_t)b * a.width;
+      auto row_at = [&](int tok) -> size_t {  // row of codes of a token (some row where there is none)
+        int page = 0;
+        if (tok < keys) {
+          page = table[tok >> plog];
+          if (page < 0 || page >= a.c.n_pages) page = 0;
+        }
+        return (((size_t)page * a.c.heads + h) << plog) + (tok & (a.c.page - 1));
+      };
+      uint4 kw[KW];
+      uint32_t vw[8][VW];
+      auto load_k = [&](int t) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.c.k + row_at(tok0 + t * kTile + kn) * D + kh * (D / 2));
+#pragma unroll
+        for (int j = 0; j < KW; ++j) kw[j] = p[j];
+      };
+      auto load_v = [&](int t) {
+        const int8_t* p = a.c.v + row_at(tok0 + t * kTile + 8 * vc) * D + vg * (D / 16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (VW == 2) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p + j * D);
+            vw[j][0] = w.x, vw[j][1] = w.y;
+          } else {
+            vw[j][0] = *reinterpret_cast<const uint32_t*>(p + j * D);
+          }
+        }
+      };
+      load_k(0);
+      load_v(0);
+      for (int t = 0; t < take; ++t) {
+        const uint32_t it = steps + t, st = it & 1u, ph = (it >> 1) & 1u;
+        wait_bounded(bar(K_EMPTY + st), ph ^ 1u, abort_flag, a.status);
+        __syncwarp();
+        const uint32_t kb = base + S::kKeys + st * S::kK;
+#pragma unroll
+        for (int j = 0; j < KW; ++j) {
+          const uint32_t w[4] = {kw[j].x ^ 0x80808080u, kw[j].y ^ 0x80808080u, kw[j].z ^ 0x80808080u,
+                                 kw[j].w ^ 0x80808080u};
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {  // eight codes: one 16-byte chunk of the row's 128-byte blocks
+            const int chunk = kh * (D / 16) + 2 * j + u;
+            sts128(kb + (chunk >> 3) * (kTile * 128) + kn * 128 + (((chunk & 7) ^ (kn & 7)) << 4),
+                   bytes2(w[2 * u], 0x4140), bytes2(w[2 * u], 0x4342), bytes2(w[2 * u + 1], 0x4140),
+                   bytes2(w[2 * u + 1], 0x4342));
+          }
+        }
+        if (ct < 4) {
+          const int tok = tok0 + t * kTile + 16 * ct;
+          float4 sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);  // a key scale of 0: no keys
+          if (tok < keys) {
+            const int page = table[tok >> plog];
+            if (page >= 0 && page < a.c.n_pages) {
+              const size_t ph_ = (size_t)page * a.c.heads + h;
+              const int ev = min(max(scale_exp(a.c.vs[ph_]), -126), 126);
+              sc = make_float4(a.c.ks[ph_], (float)ev, pow2(-ev), 0.0f);
+            } else {
+              bad_index(a.status);
+            }
+          }
+          scales[(it & 3u) * 4 + ct] = sc;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(K_FULL + st));
+        if (t + 1 < take) load_k(t + 1);
+
+        wait_bounded(bar(V_EMPTY + st), ph ^ 1u, abort_flag, a.status);
+        __syncwarp();
+        const uint32_t vb = base + S::kValues + st * S::kK;
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          uint32_t o[4][4];  // [coordinate][pair of tokens]
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t x0 = vw[2 * q][w] ^ 0x80808080u, x1 = vw[2 * q + 1][w] ^ 0x80808080u;
+            const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
+            o[0][q] = bytes2(lo, 0x4140), o[1][q] = bytes2(lo, 0x4342);
+            o[2][q] = bytes2(hi, 0x4140), o[3][q] = bytes2(hi, 0x4342);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int d = vg * (D / 16) + 4 * w + i;
+            sts128(vb + d * 128 + ((vc ^ (d & 7)) << 4), o[i][0], o[i][1], o[i][2], o[i][3]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(V_FULL + st));
+        if (t + 1 < take) load_v(t + 1);
+      }
+    } else {
+      // ---- scores, weights, products ----
+      auto scores = [&](uint32_t it) {  // warp 0
+        const uint32_t st = it & 1u;
+        wait_bounded(bar(K_FULL + st), (it >> 1) & 1u, abort_flag, a.status);
+        __syncwarp();
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t kd = desc_sw128(base + S::kKeys + st * S::kK);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ts<kTile>(tmem + kColS, tmem + kColQ + 8 * k, kd + (uint64_t)((k >> 2) * (kTile * 128 / 16) + (k & 3) * 2),
+                          k > 0);
+          if constexpr (TWO) {
+            const uint64_t ld = desc_sw128(base + S::kLow);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss<kTile>(tmem + kColS, ld + (uint64_t)((k >> 2) * (kRows * 128 / 16) + (k & 3) * 2),
+                            kd + (uint64_t)((k >> 2) * (kTile * 128 / 16) + (k & 3) * 2));
+          }
+          commit(bar(K_EMPTY + st));
+          commit(bar(S_FULL));
+        }
+        __syncwarp();
+      };
+      if (warp == 0) scores(steps);
+      const float fac = row_fac[tid];
+      const int lim = row_lim[tid];
+      float top = 0.0f, sum = 0.0f;
+      bool none = true;  // no key seen so far: the maximum says nothing
+      for (int t = 0; t < take; ++t) {
+        const uint32_t it = steps + t;
+        const int tok = tok0 + t * kTile;
+        wait_bounded(bar(S_FULL), it & 1u, abort_flag, a.status);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t v[64];
+        tmem_ld32(tmem_row + kColS, v);
+        tmem_ld32(tmem_row + kColS + 32, v + 32);
+        wait_ld();
+        float4 sc[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) sc[g] = scales[(it & 3u) * 4 + g];
+        const float was = none ? 0.0f : top;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float c = sc[g].x * fac, d = sc[g].y - was;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float x = fmaf(__uint_as_float(v[16 * g + j]), c, d);
+            v[16 * g + j] = __float_as_uint(x);
+          }
+        }
+        const bool whole = tok + kTile <= lim && sc[0].x != 0.0f && sc[1].x != 0.0f && sc[2].x != 0.0f && sc[3].x != 0.0f;
+        if (!__all_sync(0xFFFFFFFFu, whole)) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (tok + j >= lim || sc[j / 16].x == 0.0f) v[j] = 0xFF800000u;
+        }
+#pragma unroll
+        for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
+        const bool raise = mx > 8.0f || (none && mx > -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          const float up = raise ? mx : 0.0f;
+          const float f = none ? 1.0f : ex2(-up);  // nothing to rescale before the first key
+          top = was + up;
+          if (raise) none = false;
+          sum *= f;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) - up);
+          if (t > 0) {  // the sum so far stands in TMEM, and no product is under way
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tmem_row + kColO + c, o);
+              wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(tmem_row + kColO + c, o);
+            }
+          }
+        }
+        uint32_t p[32];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float part0 = 0.0f, part1 = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float e0 = ex2(__uint_as_float(v[16 * g + 2 * j])), e1 = ex2(__uint_as_float(v[16 * g + 2 * j + 1]));
+            part0 += e0, part1 += e1;
+            p[8 * g + j] = pack2<__half>(e0, e1);
+          }
+          sum = fmaf(part0 + part1, sc[g].z, sum);
+        }
+        tmem_st32(tmem_row + kColS, p);
+        wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(P_FULL));
+        if (warp == 0) {
+          const uint32_t st = it & 1u;
+          wait_bounded(bar(P_FULL), it & 1u, abort_flag, a.status);
+          wait_bounded(bar(V_FULL + st), (it >> 1) & 1u, abort_flag, a.status);
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t vd = desc_sw128(base + S::kValues + st * S::kK);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ts<D>(tmem + kColO, tmem + kColS + 8 * k, vd + (uint64_t)(2 * k), t > 0 || k > 0);
+            commit(bar(V_EMPTY + st));
+            if (t + 1 == take) commit(bar(O_FULL));
+          }
+          __syncwarp();
+          if (t + 1 < take) scores(it + 1);
+        }
+      }
+      wait_bounded(bar(O_FULL), items & 1u, abort_flag, a.status);
+      __syncwarp();
+      tc_fence_after();
+      // the rows' sums into shared memory (the stages' place), 16-byte chunks turned by the row
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tmem_row + kColO + c, o);
+        wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          sts128(base + tid * (D * 4) + (((c / 4 + j) ^ (tid & 7)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      }
+      row_stat[tid] = make_float2(none ? -INFINITY : top, sum);
+      tc_fence_before();
+    }
+    __syncthreads();
+    const bool first = t0 == 0, last = t0 + take == work;
+    const size_t slot = ((size_t)2 * cta + (first ? 1 : 0)) * kRows;
+#pragma unroll 2
+    for (int p = 0; p < kRows; p += PASS) {
+      const int r = p + tid / LPR;
+      const float4 lo = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l) ^ (r & 7)) << 4));
+      const float4 hi = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l + 1) ^ (r & 7)) << 4));
+      float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      const float2 stat = row_stat[r];
+      if (first && last) {
+        const float inv = stat.y > 0.0f ? 1.0f / stat.y : stat.y == 0.0f ? 0.0f : stat.y;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= inv;
+        uint4 w;
+        if (a.r.perm) {
+          unrotate_row<T>(x, turn, l, a.r, stage_row);
+          __syncwarp();
+          w = *reinterpret_cast<const uint4*>(stage_row + 8 * l);
+          __syncwarp();
+        } else {
+          w = pack8<T>(x);
+        }
+        const int gr = qt * kRows + r, i = gr / a.group;
+        if (r < rows)
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
+                                    ((long long)h * a.group + (gr - i * a.group)) * a.oh + 8 * l) = w;
+      } else if (r < rows) {
+        float4* o = reinterpret_cast<float4*>(a.piece + (slot + r) * D + 8 * l);
+        o[0] = lo, o[1] = hi;
+        if (l == 0) *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = stat;
+      }
+    }
+    if (first && !last) desc = make_int4((int)((at - t0 + work - 1) / sh.size) - cta + 1, b, h, qt);
+    __syncthreads();
+    steps += take;
+    ++items;
+    at += take;
+    into += take;
+  }
+  if (tid == 0) a.desc[cta] = desc;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+}
+
+template <typename T, int D, bool TWO>
+int launch(const Args& a, cudaStream_t s) {
+  auto kern = chunk_kernel<T, D, TWO>;
+  const int smem = Smem<D, TWO>::kAlloc;
+  int per_sm = 0, nsm = 0;
+  if (int rc = occupancy(reinterpret_cast<const void*>(kern), smem, kThreads, 0, &per_sm)) return rc;
+  if (int rc = sm_count(&nsm)) return rc;
+  if (per_sm < 1) return fail(OQ_ERR_UNSUPPORTED, "attention kernel does not fit");
+  // two CTAs' TMEM is an SM's, whatever else would fit
+  const long long rows = (long long)a.T * a.group;
+  const long long items = std::min<long long>((rows + kRows - 1) / kRows + a.B, rows) * a.c.heads;
+  const long long tiles = items * std::max<long long>(1, ((long long)a.width * a.c.page + kTile - 1) / kTile);
+  const int ctas = (int)std::min<long long>(tiles, std::min(nsm * std::min(per_sm, 2), kChunkCtas));
+  kern<<<ctas, kThreads, smem, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+  join_kernel<T, D, kRows><<<dim3((unsigned)ctas, 16), 128, 0, s>>>(a, 0);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention join launch: %s", cudaGetErrorString(e));
+  return OQ_OK;
+}
+
+}  // namespace
+
+int launch_cattn_chunk(const cattn::Args& a, int dtype, int d, void* stream) {
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == OQ_BF16) return d == 128 ? launch<__nv_bfloat16, 128, false>(a, s) : launch<__nv_bfloat16, 64, false>(a, s);
+  // fp16 rows that are not turned are exact in one term
+  if (!a.r.perm) return d == 128 ? launch<__half, 128, false>(a, s) : launch<__half, 64, false>(a, s);
+  return d == 128 ? launch<__half, 128, true>(a, s) : launch<__half, 64, true>(a, s);
+}
+
+}  // namespace oq

@@ -360,10 +360,15 @@ def check_attention(oq, cache, bt, q, r, rot, causal, scale=None, empty_page=Non
         empty = None
         if empty_page is not None:
             empty = np.array([[scales[0][bt.table[b][t // bt.page], h] == 0 for h in range(cache.heads)]
-                              for t in range(bt.total[b])]).reshape(bt.total[b], cache.heads)
+                              for t in range(bt.total[b])], dtype=bool).reshape(bt.total[b], cache.heads)
         want, bound = oc.attention(f64(q[bt.cu[b]:bt.cu[b + 1]]), k, v, causal,
                                    q.shape[2] ** -0.5 if scale is None else scale, rot, empty)
         got = f64(out[bt.cu[b]:bt.cu[b + 1]])
+        # a value at or above the type's largest number plus half its last step (fp16: 65520) rounds to
+        # infinity: right wherever the exact value is that large within the row's bound
+        most = torch.finfo(q.dtype).max
+        over = np.isinf(got) & (np.sign(got) * want + bound[..., None] >= most * (1 + eps / 4))
+        got = np.where(over, want, got)
         err = np.linalg.norm(got - want, axis=-1)
         limit = bound + (eps / 2 + 8 * 2.0 ** -24) * 1.01 * np.linalg.norm(want, axis=-1)
         assert np.all(err <= limit), (b, (err / np.maximum(limit, 1e-300)).max())
@@ -383,6 +388,11 @@ ATTN = [  # new, past, heads, group, d, page, block, dtype, causal
     ([129, 40], [70, 0], 2, 1, 128, 16, 128, "bf16", True),
     ([129, 40], [70, 11], 1, 4, 128, 64, 0, "bf16", False),
     ([300], [0], 1, 2, 64, 128, 64, "bf16", True),
+    ([33], [0], 2, 1, 128, 16, 128, "fp16", True),
+    ([17, 0, 150, 2], [0, 20, 900, 1500], 2, 3, 128, 64, 64, "fp16", True),
+    ([200, 9], [130, 64], 1, 5, 64, 32, 0, "fp16", False),
+    ([64], [2000], 3, 2, 64, 128, 64, "bf16", False),
+    ([128, 128], [0, 128], 1, 1, 128, 32, 128, "bf16", True),
 ]
 
 
@@ -396,23 +406,34 @@ def test_attention(oq, new, past, heads, group, d, page, block, dt, causal):
     check_attention(oq, cache, bt, fused[:, 1:1 + heads * group], r, rot, causal)
 
 
-def test_attention_scales_far_apart(oq):
+@pytest.mark.parametrize("new", [[1, 2], [40, 20]])
+def test_attention_scales_far_apart(oq, new):
     """Pages whose values differ by many powers of two, and the score's own range."""
     rng = np.random.default_rng(21)
     r, rot = rotation(oq, 64, 64)
-    bt = Batch(rng, [1, 2], [200, 90], 16)
+    bt = Batch(rng, new, [200, 90], 16)
     cache = filled(oq, rng, bt, 1, 64, r)
     cache.v_scale *= torch.exp2(torch.from_numpy(rng.integers(-12, 13, (bt.n_pages, 1))).cuda()).float()
     cache.k_scale *= torch.exp2(torch.from_numpy(rng.integers(-3, 2, (bt.n_pages, 1))).cuda()).float()
     for scale in (None, 0.0, -0.3, 2.0):
-        check_attention(oq, cache, bt, rows(rng, (3, 2, 64), "fp16", loud=False), r, rot, True, scale)
-    q = rows(rng, (3, 2, 64), "bf16", loud=False)
+        check_attention(oq, cache, bt, rows(rng, (sum(new), 2, 64), "fp16", loud=False), r, rot, True, scale)
+    q = rows(rng, (sum(new), 2, 64), "bf16", loud=False)
     for f in (1e-30, 1e25):  # a query's own power of two
         check_attention(oq, cache, bt, q * f, r, rot, True, 0.1 / f)
 
 
 def test_attention_rows_without_keys(oq):
     rng = np.random.default_rng(22)
+    bt = Batch(rng, [100, 30, 20], [0, 0, 4], 16)  # many rows
+    bt.total = [70, 0, 6]
+    cache = filled(oq, rng, bt, 2, 64, None)
+    q = rows(rng, (150, 4, 64), "bf16")
+    out = check_attention(oq, cache, bt, q, None, None, True)
+    assert not out[:30].any() and out[30:100].any() and not out[100:130].any()
+    cache.k_scale[bt.table[0, 1]] = 0
+    cache.k_scale[bt.table[2, 0]] = 0
+    out = check_attention(oq, cache, bt, q, None, None, True, empty_page=True)
+    assert out[30:100].any() and not out[100:].any()
     bt = Batch(rng, [5, 3, 2], [0, 0, 4], 16)
     bt.total = [2, 0, 6]  # fewer tokens than queries; none at all
     cache = filled(oq, rng, bt, 2, 64, None)
@@ -430,12 +451,13 @@ def test_attention_rows_without_keys(oq):
     assert out[0].any() and not out[1].any()
 
 
-def test_attention_nan_query_stays_in_its_row(oq):
+@pytest.mark.parametrize("n", [3, 70])
+def test_attention_nan_query_stays_in_its_row(oq, n):
     rng = np.random.default_rng(23)
     r, rot = rotation(oq, 128, 128)
-    bt = Batch(rng, [3], [700], 64)
+    bt = Batch(rng, [n], [700], 64)
     cache = filled(oq, rng, bt, 1, 128, r)
-    q = rows(rng, (3, 2, 128), "bf16")
+    q = rows(rng, (n, 2, 128), "bf16")
     clean = oq.cache_attention(cache, q, ints(bt.cu), ints(bt.total), ints(bt.table), rpbh=r)
     q[1, 1, 5] = float("nan")
     out = oq.cache_attention(cache, q, ints(bt.cu), ints(bt.total), ints(bt.table), rpbh=r)
@@ -444,13 +466,14 @@ def test_attention_nan_query_stays_in_its_row(oq):
     assert torch.equal(out, clean)
 
 
-def test_attention_ignores_what_it_may_not_see(oq):
+@pytest.mark.parametrize("new,past", [([1, 6], [21, 77]), ([2, 60], [20, 23])])
+def test_attention_ignores_what_it_may_not_see(oq, new, past):
     """Codes behind the last token, other pages and their scales change nothing."""
     rng = np.random.default_rng(24)
     r, rot = rotation(oq, 64, 64)
-    bt = Batch(rng, [1, 6], [21, 77], 32)
+    bt = Batch(rng, new, past, 32)
     cache = filled(oq, rng, bt, 2, 64, r)
-    q = rows(rng, (7, 4, 64), "bf16")
+    q = rows(rng, (sum(new), 4, 64), "bf16")
     args = (ints(bt.cu), ints(bt.total), ints(bt.table))
     clean = oq.cache_attention(cache, q, *args, rpbh=r)
     used = {int(bt.table[b, s]) for b in range(2) for s in range(-(-bt.total[b] // 32))}

@@ -54,10 +54,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(20000)  // may sleep for up to 20 us
       : "memory");
   return ok != 0;
 }
@@ -169,6 +169,69 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* v) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+__device__ __forceinline__ unsigned long long f2_pack(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ unsigned long long u2_pack(uint32_t lo, uint32_t hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_split(unsigned long long v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b,
+                                                     unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A row's weights 2^(score + ev - top) of 64 keys from its scores in TMEM, as
+// fp16 pairs; `part`: their sums in groups of 16 keys; `mx`: the largest exponent.
+// MASKED: only the first `left` keys are seen.
+template <bool MASKED>
+__device__ __forceinline__ void weigh(uint32_t scores, const float4 (&sc)[4], float fac, float top, int left,
+                                      uint32_t (&p)[32], float (&part)[4], float& mx) {
+  mx = -INFINITY;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t v[32];
+    tmem_ld32(scores + 32 * hf, v);
+    wait_ld();
+#pragma unroll
+    for (int gg = 0; gg < 2; ++gg) {
+      const int g = 2 * hf + gg;
+      const float c = sc[g].x * fac, d = sc[g].x != 0.0f ? sc[g].y - top : -INFINITY;  // an empty page's scores go
+      const unsigned long long c2 = f2_pack(c, c), d2 = f2_pack(d, d);
+      unsigned long long add = f2_pack(0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float x0, x1;
+        f2_split(f2_fma(u2_pack(v[16 * gg + 2 * j], v[16 * gg + 2 * j + 1]), c2, d2), x0, x1);
+        if constexpr (MASKED) {
+          if (16 * g + 2 * j >= left) x0 = -INFINITY;
+          if (16 * g + 2 * j + 1 >= left) x1 = -INFINITY;
+        }
+        mx = fmaxf(mx, fmaxf(x0, x1));
+        const float e0 = ex2(x0), e1 = ex2(x1);
+        add = f2_add(add, f2_pack(e0, e1));
+        p[8 * g + j] = pack2<__half>(e0, e1);
+      }
+      float s0, s1;
+      f2_split(add, s0, s1);
+      part[g] = s0 + s1;
+    }
+  }
 }
 
 template <int D, bool TWO>
@@ -365,8 +428,23 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
           }
         }
       };
+      float4 sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
+      auto load_scales = [&](int t) {  // four threads, a group of 16 tokens each
+        const int tok = tok0 + t * kTile + 16 * ct;
+        sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);  // a key scale of 0: no keys
+        if (tok < keys) {
+          const int page = table[tok >> plog];
+          if (page >= 0 && page < a.c.n_pages) {
+            const size_t ph = (size_t)page * a.c.heads + h;
+            sc.x = a.c.ks[ph], sc.y = a.c.vs[ph];
+          } else {
+            bad_index(a.status);
+          }
+        }
+      };
       load_k(0);
       load_v(0);
+      if (ct < 4) load_scales(0);
       for (int t = 0; t < take; ++t) {
         const uint32_t it = steps + t, st = it & 1u, ph = (it >> 1) & 1u;
         wait_bounded(bar(K_EMPTY + st), ph ^ 1u, abort_flag, a.status);
@@ -385,24 +463,16 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
           }
         }
         if (ct < 4) {
-          const int tok = tok0 + t * kTile + 16 * ct;
-          float4 sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);  // a key scale of 0: no keys
-          if (tok < keys) {
-            const int page = table[tok >> plog];
-            if (page >= 0 && page < a.c.n_pages) {
-              const size_t ph_ = (size_t)page * a.c.heads + h;
-              const int ev = min(max(scale_exp(a.c.vs[ph_]), -126), 126);
-              sc = make_float4(a.c.ks[ph_], (float)ev, pow2(-ev), 0.0f);
-            } else {
-              bad_index(a.status);
-            }
-          }
-          scales[(it & 3u) * 4 + ct] = sc;
+          const int ev = min(max(scale_exp(sc.y), -126), 126);
+          scales[(it & 3u) * 4 + ct] = make_float4(sc.x, (float)ev, pow2(-ev), 0.0f);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(K_FULL + st));
-        if (t + 1 < take) load_k(t + 1);
+        if (t + 1 < take) {
+          load_k(t + 1);
+          if (ct < 4) load_scales(t + 1);
+        }
 
         wait_bounded(bar(V_EMPTY + st), ph ^ 1u, abort_flag, a.status);
         __syncwarp();
@@ -464,41 +534,32 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
         wait_bounded(bar(S_FULL), it & 1u, abort_flag, a.status);
         __syncwarp();
         tc_fence_after();
-        uint32_t v[64];
-        tmem_ld32(tmem_row + kColS, v);
-        tmem_ld32(tmem_row + kColS + 32, v + 32);
-        wait_ld();
         float4 sc[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) sc[g] = scales[(it & 3u) * 4 + g];
-        const float was = none ? 0.0f : top;
-        float mx = -INFINITY;
+        // The weights at once, against the maximum so far; in the rare step that
+        // raises it (2^8 and more above, or the first keys of a row) once more
+        // from the scores, which still stand in TMEM.
+        uint32_t p[32];
+        const int left = lim - tok;  // keys of the step that the row may see
+        const bool whole = __all_sync(0xFFFFFFFFu, left >= kTile);
+        for (int tries = 0; tries < 2; ++tries) {
+          float mx, part[4];
+          if (whole)
+            weigh<false>(tmem_row + kColS, sc, fac, top, left, p, part, mx);
+          else
+            weigh<true>(tmem_row + kColS, sc, fac, top, left, p, part, mx);
+          const bool raise = mx > 8.0f || (none && mx > -INFINITY);
+          if (tries > 0 || !__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float c = sc[g].x * fac, d = sc[g].y - was;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float x = fmaf(__uint_as_float(v[16 * g + j]), c, d);
-            v[16 * g + j] = __float_as_uint(x);
+            for (int g = 0; g < 4; ++g) sum = fmaf(part[g], sc[g].z, sum);
+            break;
           }
-        }
-        const bool whole = tok + kTile <= lim && sc[0].x != 0.0f && sc[1].x != 0.0f && sc[2].x != 0.0f && sc[3].x != 0.0f;
-        if (!__all_sync(0xFFFFFFFFu, whole)) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (tok + j >= lim || sc[j / 16].x == 0.0f) v[j] = 0xFF800000u;
-        }
-#pragma unroll
-        for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
-        const bool raise = mx > 8.0f || (none && mx > -INFINITY);
-        if (__any_sync(0xFFFFFFFFu, raise)) {
           const float up = raise ? mx : 0.0f;
           const float f = none ? 1.0f : ex2(-up);  // nothing to rescale before the first key
-          top = was + up;
+          top += up;
           if (raise) none = false;
           sum *= f;
-#pragma unroll
-          for (int j = 0; j < 64; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) - up);
           if (t > 0) {  // the sum so far stands in TMEM, and no product is under way
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -510,18 +571,6 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
               tmem_st16(tmem_row + kColO + c, o);
             }
           }
-        }
-        uint32_t p[32];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float part0 = 0.0f, part1 = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float e0 = ex2(__uint_as_float(v[16 * g + 2 * j])), e1 = ex2(__uint_as_float(v[16 * g + 2 * j + 1]));
-            part0 += e0, part1 += e1;
-            p[8 * g + j] = pack2<__half>(e0, e1);
-          }
-          sum = fmaf(part0 + part1, sc[g].z, sum);
         }
         tmem_st32(tmem_row + kColS, p);
         wait_st();
@@ -618,11 +667,12 @@ int launch(const Args& a, cudaStream_t s) {
   if (int rc = occupancy(reinterpret_cast<const void*>(kern), smem, kThreads, 0, &per_sm)) return rc;
   if (int rc = sm_count(&nsm)) return rc;
   if (per_sm < 1) return fail(OQ_ERR_UNSUPPORTED, "attention kernel does not fit");
-  // two CTAs' TMEM is an SM's, whatever else would fit
+  // two CTAs share an SM's registers, shared memory and TMEM by construction (the
+  // occupancy query says one for a kernel that allocates TMEM); none waits for another
   const long long rows = (long long)a.T * a.group;
   const long long items = std::min<long long>((rows + kRows - 1) / kRows + a.B, rows) * a.c.heads;
   const long long tiles = items * std::max<long long>(1, ((long long)a.width * a.c.page + kTile - 1) / kTile);
-  const int ctas = (int)std::min<long long>(tiles, std::min(nsm * std::min(per_sm, 2), kChunkCtas));
+  const int ctas = (int)std::min<long long>(tiles, std::min(2 * nsm, kChunkCtas));
   kern<<<ctas, kThreads, smem, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));

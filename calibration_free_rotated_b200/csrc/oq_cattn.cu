@@ -5,8 +5,9 @@
 // on codes: k_j = 2^ek ck_j, v_j = 2^ev cv_j with one ek, ev for a page and head.
 // The turned query stands in fp16 beside a power of two of its own (largest
 // value in [1, 2), so no range is lost; each value is rounded by at most 2^-12
-// of itself, a sixteenth of a bf16 rounding), the codes are exact in fp16, sums
-// are fp32.
+// of itself, a sixteenth of a bf16 rounding; for fp16 tensors, where that would
+// show, what the rounding leaves out is a second term), the codes are exact in
+// fp16, sums are fp32.
 //
 // The running maximum is taken over score + ev (logarithms to base 2), so the
 // weights p * 2^ev that go to fp16 are at most 2^8 and right to 2^-12 where they
@@ -41,6 +42,8 @@ using namespace cattn;
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kStages = 4;
+constexpr int kTile = 64;  // keys of a tile: 16 for each warp
+constexpr int kStart = 2;  // units of an item's beginning and end
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -77,14 +80,15 @@ __device__ __forceinline__ int value_at(int row, int chunk) {
                   : (row >> 1) * 128 + (((row ^ (row >> 1)) & 1) << 6) + ((chunk ^ (((row >> 2) & 1) << 1)) << 4);
 }
 
-template <int D, int NQ>
+template <int D, int NQ, bool TWO>
 struct Smem {
   static constexpr int RT = 8 * NQ;
   static constexpr int kStageBytes = 2 * 16 * D;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kScales = kRing;                             // [warps][stages][2] floats
   static constexpr int kQ = kScales + kWarps * kStages * 8;         // [RT][D + 8] halves
-  static constexpr int kRow = kQ + RT * (D + 8) * 2;                // [RT] factor, [RT] limit
+  static constexpr int kLow = kQ + RT * (D + 8) * 2;                // the same: the query's second term
+  static constexpr int kRow = kLow + (TWO ? RT * (D + 8) * 2 : 0);  // [RT] factor, [RT] limit
   static constexpr int kStat = kRow + RT * 8;                       // [warps][RT] maximum, sum
   static constexpr int kStageRow = kStat + kWarps * RT * 8;         // [128 / (D / 8)][D] 16-bit rows
   static constexpr int kTotal = kStageRow + kThreads / (D / 8) * D * 2;
@@ -93,16 +97,17 @@ struct Smem {
   static_assert(kQ % 16 == 0 && kRow % 16 == 0 && kStat % 16 == 0 && kStageRow % 16 == 0, "alignment");
 };
 
-template <typename T, int D, int NQ>
+template <typename T, int D, int NQ, bool TWO>
 __global__ void __launch_bounds__(kThreads, NQ == 1 ? 3 : 2)
 step_kernel(const __grid_constant__ Args a) {
-  using S = Smem<D, NQ>;
+  using S = Smem<D, NQ, TWO>;
   constexpr int RT = S::RT, LPR = D / 8, KS = D / 16;
   extern __shared__ __align__(16) unsigned char sm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int cta = blockIdx.x;
   __half* qs = reinterpret_cast<__half*>(sm + S::kQ);
+  __half* low = reinterpret_cast<__half*>(sm + S::kLow);
   float* row_fac = reinterpret_cast<float*>(sm + S::kRow);
   int* row_lim = reinterpret_cast<int*>(sm + S::kRow + RT * 4);
   float* w_max = reinterpret_cast<float*>(sm + S::kStat);
@@ -113,7 +118,7 @@ step_kernel(const __grid_constant__ Args a) {
   const float* scales_p = reinterpret_cast<const float*>(sm + S::kScales) + warp * kStages * 2;
   const uint32_t scales_s = smem_u32(sm) + S::kScales + warp * kStages * 8;
 
-  const Share sh = find_share<RT, kThreads>(a, cta, gridDim.x);
+  const Share sh = find_share<RT, kTile, kStart, kThreads>(a, cta, gridDim.x);
   long long at = sh.size * cta;
   const long long stop = min(sh.total, at + sh.size);
   int4 desc = make_int4(0, 0, 0, 0);
@@ -125,28 +130,30 @@ step_kernel(const __grid_constant__ Args a) {
 
   while (at < stop && b < a.B) {
     const Seq s = load_seq(a, b, false);
-    const long long per_head = head_work<RT>(a, s);
+    const long long per_head = units_before<RT, kTile, kStart>(a, s, row_tiles<RT>(s));
     if (into >= per_head * a.c.heads) {
       ++b;
       into = 0;
       continue;
     }
-    const int h = (int)(into / per_head);
-    long long rem = into - h * per_head;
-    int qt = 0, work = tile_work<RT>(a, s, 0);
-    while (rem >= work) {
-      rem -= work;
-      work = tile_work<RT>(a, s, ++qt);
+    const Part part = find_part<RT, kTile, kStart>(a, s, per_head, into, stop - at);
+    const int h = part.h, qt = part.qt, keys = part.keys, t0 = part.t0, take = part.t1 - part.t0;
+    const bool first = t0 == 0, last = part.t1 == part.tiles;
+    const size_t slot = ((size_t)2 * cta + (first ? 1 : 0)) * RT;
+    const long long item_end = at - into + part.end;
+    at += part.units;
+    into += part.units;
+    if (take == 0) {  // no key tile: nothing to do, but a piece that the join counts on says so
+      if (t0 > 0 && threadIdx.x < RT) *reinterpret_cast<float2*>(a.stat + 2 * (slot + threadIdx.x)) = make_float2(-INFINITY, 0.0f);
+      continue;
     }
-    const int t0 = (int)rem, take = (int)min((long long)(work - t0), stop - at);
-    const int keys = tile_keys<RT>(a, s, qt);
     const int rows = min(RT, s.rows - qt * RT);
 
     // the item's query rows: turned, scaled by a power of two, fp16
 #pragma unroll
     for (int p = 0; p < RT; p += kThreads / LPR) {
       const int r = p + threadIdx.x / LPR;
-      const int gr = qt * RT + min(r, rows - 1), i = gr / a.group;
+      const int gr = qt * RT + min(r, rows - 1), i = row_token(a, gr);
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows)
         w = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + i) * a.qt +
@@ -170,7 +177,15 @@ step_kernel(const __grid_constant__ Args a) {
         const float f = pow2(-e);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] *= f;
-        *reinterpret_cast<uint4*>(qs + r * (D + 8) + 8 * l) = pack8<__half>(x);
+        const uint4 hi = pack8<__half>(x);
+        *reinterpret_cast<uint4*>(qs + r * (D + 8) + 8 * l) = hi;
+        if constexpr (TWO) {
+          float y[8];
+          unpack8<__half>(hi, y);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = x[k] - y[k];
+          *reinterpret_cast<uint4*>(low + r * (D + 8) + 8 * l) = pack8<__half>(y);
+        }
         if (l == 0) {
           row_fac[r] = pow2(e) * a.scale;
           row_lim[r] = r >= rows ? 0 : a.causal ? s.len - s.n + i + 1 : s.len;
@@ -261,7 +276,13 @@ step_kernel(const __grid_constant__ Args a) {
           const uint32_t a0 = bytes2(x0, 0x4140), a1 = bytes2(x1, 0x4140), a2 = bytes2(x0, 0x4342),
                          a3 = bytes2(x1, 0x4342);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) mma16816(sc[n], a0, a1, a2, a3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
+          for (int n = 0; n < NQ; ++n) {
+            mma16816(sc[n], a0, a1, a2, a3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
+            if constexpr (TWO) {
+              const uint2 w = *reinterpret_cast<const uint2*>(low + (8 * n + g) * (D + 8) + 64 * j + 16 * c + 4 * i);
+              mma16816(sc[n], a0, a1, a2, a3, w.x, w.y);
+            }
+          }
         }
       }
       // scores to base 2 plus the values' exponent; rows of sc: tokens g, g + 8; columns: rows 2 c, 2 c + 1
@@ -358,8 +379,6 @@ step_kernel(const __grid_constant__ Args a) {
       }
     }
     __syncthreads();
-    const bool first = t0 == 0, last = t0 + take == work;
-    const size_t slot = ((size_t)2 * cta + (first ? 1 : 0)) * RT;
 #pragma unroll
     for (int p = 0; p < RT; p += kThreads / LPR) {
       const int r = p + threadIdx.x / LPR, rr = min(r, RT - 1);
@@ -391,7 +410,7 @@ step_kernel(const __grid_constant__ Args a) {
         } else {
           w = pack8<T>(x);
         }
-        const int gr = qt * RT + r, i = gr / a.group;
+        const int gr = qt * RT + r, i = row_token(a, gr);
         if (r < rows)
           *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
                                     ((long long)h * a.group + (gr - i * a.group)) * a.oh + 8 * l) = w;
@@ -399,14 +418,12 @@ step_kernel(const __grid_constant__ Args a) {
         float4* o = reinterpret_cast<float4*>(a.piece + (slot + r) * D + 8 * l);
         o[0] = make_float4(x[0], x[1], x[2], x[3]);
         o[1] = make_float4(x[4], x[5], x[6], x[7]);
-        if (l == 0) *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = make_float2(mx, total);
+        if (l == 0)  // (a NaN query leaves no maximum; its piece must count all the same)
+          *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = make_float2(total == total ? mx : 0.0f, total);
       }
     }
-    if (first && !last)
-      desc = make_int4((int)((at - t0 + work - 1) / sh.size) - cta + 1, b, h, qt);
+    if (first && !last) desc = make_int4((int)((item_end - 1) / sh.size) - cta + 1, b, h, qt);
     __syncthreads();
-    at += take;
-    into += take;
   }
   if (threadIdx.x == 0) a.desc[cta] = desc;
 }
@@ -426,10 +443,10 @@ Plan plan_of(int T, int B, int group) {
 size_t piece_bytes(const Plan& p, int d) { return sizeof(float) * 2 * (size_t)p.ctas * p.rows * d; }
 size_t stat_bytes(const Plan& p) { return sizeof(float) * 4 * (size_t)p.ctas * p.rows; }
 
-template <typename T, int D, int NQ>
+template <typename T, int D, int NQ, bool TWO>
 int launch_step(const Args& a, int ctas_most, cudaStream_t s) {
-  auto kern = step_kernel<T, D, NQ>;
-  const int smem = Smem<D, NQ>::kTotal;
+  auto kern = step_kernel<T, D, NQ, TWO>;
+  const int smem = Smem<D, NQ, TWO>::kTotal;
   int per_sm = 0, nsm = 0;
   if (int rc = occupancy(reinterpret_cast<const void*>(kern), smem, kThreads, 0, &per_sm)) return rc;
   if (int rc = sm_count(&nsm)) return rc;
@@ -468,6 +485,7 @@ int launch_cattn(const AttnCall& c) {
   a.cu = c.cu, a.lens = c.lens, a.table = c.table;
   a.B = c.B, a.T = c.T, a.width = c.width;
   a.group = c.heads / v->heads;
+  a.div_group = a.group > 1 ? (unsigned)((0x100000000ull + a.group - 1) / a.group) : 0u;
   a.causal = c.causal;
   a.scale = (float)((double)c.scale * 1.4426950408889634);
   const Plan p = plan_of(c.T, c.B, a.group);
@@ -476,13 +494,18 @@ int launch_cattn(const AttnCall& c) {
   a.desc = reinterpret_cast<int4*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d) + stat_bytes(p));
   if (p.rows == 128) return launch_cattn_chunk(a, c.dtype, v->d, c.stream);
   cudaStream_t s = (cudaStream_t)c.stream;
-#define OQ_STEP(T, D) return p.rows == 8 ? launch_step<T, D, 1>(a, p.ctas, s) : launch_step<T, D, 2>(a, p.ctas, s)
+#define OQ_STEP(T, D, TWO) \
+  return p.rows == 8 ? launch_step<T, D, 1, TWO>(a, p.ctas, s) : launch_step<T, D, 2, TWO>(a, p.ctas, s)
   if (c.dtype == OQ_BF16) {
-    if (v->d == 128) OQ_STEP(__nv_bfloat16, 128);
-    OQ_STEP(__nv_bfloat16, 64);
+    if (v->d == 128) OQ_STEP(__nv_bfloat16, 128, false);
+    OQ_STEP(__nv_bfloat16, 64, false);
   }
-  if (v->d == 128) OQ_STEP(__half, 128);
-  OQ_STEP(__half, 64);
+  if (!a.r.perm) {  // fp16 rows that are not turned are exact in one term
+    if (v->d == 128) OQ_STEP(__half, 128, false);
+    OQ_STEP(__half, 64, false);
+  }
+  if (v->d == 128) OQ_STEP(__half, 128, true);
+  OQ_STEP(__half, 64, true);
 #undef OQ_STEP
 }
 

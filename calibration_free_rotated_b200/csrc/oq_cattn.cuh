@@ -3,18 +3,22 @@
 //
 // An item is (sequence, head of the cache, tile of query rows): the rows of a
 // tile are the new tokens' query heads that share the cache's head, row r being
-// token r / group, head r % group of the group.  An item's work is its number of
-// key tiles.  The items' tiles in a row (sequence, head, row tile) are cut into
+// token r / group, head r % group of the group.  An item walks its key tiles.
+// Its work is counted in units: a fixed number for its beginning and end (the
+// query's turn, the first loads, the rows' turn back) and about one for each key
+// tile.  The units of all items in a row (sequence, head, row tile) are cut into
 // equal shares, one for each CTA, wherever the cut falls, so that ragged batches
 // and a single long stream fill the machine alike.  A CTA finds its share from
-// the lengths on the device: nothing about them is known on the host.
+// the lengths on the device: nothing about them is known on the host.  How many
+// units the first q row tiles of a head have is a closed form (units_before), so
+// no CTA walks over items that are not its own.
 //
 // An item that one CTA covers is finished there.  Of an item that is cut, each
 // CTA leaves a piece in the workspace (for each row its running maximum, sum and
-// weighted values, fp32): the CTA that begins it in its slot 1, the ones that go
-// on with it in their slot 0.  The beginning CTA also writes down which CTAs hold
-// pieces, and the joining kernel adds them up in the CTAs' order: no atomics, the
-// same result every time.
+// weighted values, fp32): the CTA that has the first key tile in its slot 1, the
+// ones that go on with it in their slot 0.  The first also writes down which CTAs
+// hold pieces, and the joining kernel adds them up in the CTAs' order: no
+// atomics, the same result every time.
 #pragma once
 
 #include "oq_cache.cuh"
@@ -24,7 +28,6 @@ namespace cattn {
 
 using namespace cache;
 
-constexpr int kTile = 64;  // keys of a tile: the unit of work
 // Most CTAs that the workspace has pieces for (the kernels' residency on 148 SMs).
 constexpr int kStepCtas = 148 * 4, kChunkCtas = 148 * 2;
 
@@ -42,6 +45,7 @@ struct Args {
   float* stat;    // [2 ctas][rows of a tile][2]: maximum, sum
   int4* desc;     // [ctas]: (pieces, sequence, head, row tile)
   int B, T, width, group, causal;
+  unsigned div_group;  // 2^32 / group, rounded up (group > 1)
   float scale;    // of the scores, times log2(e)
 };
 
@@ -63,35 +67,43 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int b, bool report) {
   s.rows = s.n * a.group;
   return s;
 }
+// Token of a row: r / group.
+__device__ __forceinline__ int row_token(const Args& a, int r) {
+  if (a.group == 1) return r;
+  const int q = (int)__umulhi((unsigned)r, a.div_group);  // right, or one too many
+  return (long long)q * a.group > r ? q - 1 : q;
+}
 // Keys that the row tile's last row may see (causal: the tile's other rows see no more).
 template <int RT>
 __device__ __forceinline__ int tile_keys(const Args& a, const Seq& s, int qt) {
   if (!a.causal) return s.len;
-  const int last = min(s.rows - 1, qt * RT + RT - 1) / a.group;
-  return max(0, s.len - s.n + last + 1);
+  return max(0, s.len - s.n + row_token(a, min(s.rows - 1, qt * RT + RT - 1)) + 1);
 }
 template <int RT>
-__device__ __forceinline__ int tile_work(const Args& a, const Seq& s, int qt) {
-  return max(1, (tile_keys<RT>(a, s, qt) + kTile - 1) / kTile);
+__device__ __forceinline__ int row_tiles(const Seq& s) {
+  return (s.rows + RT - 1) / RT;
 }
-template <int RT>
-__device__ __forceinline__ long long head_work(const Args& a, const Seq& s) {
-  const int tiles = (s.rows + RT - 1) / RT;
-  if (!a.causal || tiles <= 1) return tiles ? (long long)tiles * tile_work<RT>(a, s, 0) : 0;
-  long long w = 0;
-  for (int qt = 0; qt < tiles; ++qt) w += tile_work<RT>(a, s, qt);
-  return w;
+// Units of the first q row tiles of a head: START each, and the key tiles (for
+// causal rows a smooth count, right but for roundings: row tile i sees
+// len - n + (i + 1) RT / group keys).
+template <int RT, int TILE, int START>
+__device__ __forceinline__ long long units_before(const Args& a, const Seq& s, int q) {
+  if (!a.causal) return (long long)q * (START + max(1, (s.len + TILE - 1) / TILE));
+  const unsigned long long num = (unsigned long long)q * (2ull * a.group * max(0, s.len - s.n) + (unsigned long long)RT * (q + 1));
+  const unsigned den = 2u * a.group * TILE;
+  const unsigned long long tiles = num >> 32 ? num / den : (unsigned)num / den;
+  return (long long)q * (START + 1) + (long long)tiles;
 }
 
 // Where a CTA's share begins.
 struct Share {
-  long long total, size;  // tiles of all items, of a share
-  int b;                  // sequence of the first tile; B when the share is empty
-  long long into;         // tiles of that sequence before it
+  long long total, size;  // units of all items, of a share
+  int b;                  // sequence of the first unit; B when the share is empty
+  long long into;         // units of that sequence before it
 };
 
 // All THREADS threads of the CTA take part and get the same answer.
-template <int RT, int THREADS>
+template <int RT, int TILE, int START, int THREADS>
 __device__ Share find_share(const Args& a, int cta, int ctas) {
   __shared__ long long warp_sum[THREADS / 32];
   __shared__ Share found;
@@ -108,7 +120,7 @@ __device__ Share find_share(const Args& a, int cta, int ctas) {
         mine = 0;
         if (b < a.B) {
           const Seq s = load_seq(a, b, pass == 0 && cta == 0);
-          mine = head_work<RT>(a, s) * a.c.heads;
+          mine = units_before<RT, TILE, START>(a, s, row_tiles<RT>(s)) * a.c.heads;
         }
       }
       long long incl = mine;
@@ -143,6 +155,47 @@ __device__ Share find_share(const Args& a, int cta, int ctas) {
   return s;
 }
 
+// The part of an item that a CTA has.
+struct Part {
+  int h, qt;          // head, row tile
+  int keys, tiles;    // keys and key tiles of the item
+  int t0, t1;         // key tiles of the part; none: t0 == t1
+  long long units;    // how far the share goes on
+  long long end;      // units of the sequence up to the item's end
+};
+// `into`: units of sequence s before the part, `left`: units of the share from there on.
+template <int RT, int TILE, int START>
+__device__ __forceinline__ Part find_part(const Args& a, const Seq& s, long long per_head, long long into, long long left) {
+  Part p;
+  p.h = (int)(into / per_head);
+  const long long rem = into - p.h * per_head;
+  int lo = 0, hi = row_tiles<RT>(s);  // units_before(lo) <= rem < units_before(hi)
+  long long before = 0, after = per_head;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    const long long u = units_before<RT, TILE, START>(a, s, mid);
+    if (u <= rem) {
+      lo = mid, before = u;
+    } else {
+      hi = mid, after = u;
+    }
+  }
+  p.qt = lo;
+  p.keys = tile_keys<RT>(a, s, lo);
+  p.tiles = max(1, (p.keys + TILE - 1) / TILE);
+  const long long item = after - before, at = rem - before;
+  p.units = min(item - at, left);
+  p.end = into - at + item;
+  // the units behind the first START stand for the key tiles, in proportion
+  const long long u0 = max(0ll, at - START), u1 = max(0ll, at + p.units - START), span = item - START;
+  if (span == p.tiles) {
+    p.t0 = (int)u0, p.t1 = (int)u1;
+  } else {
+    p.t0 = (int)(u0 * p.tiles / span), p.t1 = (int)(u1 * p.tiles / span);
+  }
+  return p;
+}
+
 // Puts the pieces of cut items together and writes their rows: block (i, j) the
 // rows j, j + gridDim.y, ... of the item that CTA i began.
 template <typename T, int D, int RT>
@@ -174,6 +227,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     for (int i = warp; i < d.x; i += 4) {
       const size_t at = slot(i);
       const float f = exp2f(a.stat[2 * at] - top);
+      if (f == 0.0f) continue;  // nothing there: its values may not even be written
       sum = fmaf(f, a.stat[2 * at + 1], sum);
       const float* p = a.piece + at * D + V * lane;
       if constexpr (V == 4) {
@@ -204,7 +258,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
       } else {
         w = pack8<T>(x);
       }
-      const int g = d.w * RT + r, i = g / a.group;
+      const int g = d.w * RT + r, i = row_token(a, g);
       if (lane < D / 8)
         *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
                                   ((long long)d.z * a.group + (g - i * a.group)) * a.oh + 8 * l) = w;

@@ -2,27 +2,31 @@
 // whole images): bound by the tensor cores and what feeds them.
 //
 // The same sums as oq_cattn.cu, on tcgen05: a CTA takes 128 query rows and walks
-// 64 keys a step.  Two roles of four warps:
+// KT keys a step.  Three roles:
 //   warps 4..7  expand the step's codes to fp16 (exact) into the K-major
 //               128-byte-swizzled layout of the tensor cores' operands, the keys
-//               as they lie, the values transposed by byte permutes; two stages
-//               each, the codes of the next step already in registers.
+//               as they lie, the values transposed by byte permutes, 64 keys at
+//               a time with the codes of what comes next already in registers.
+//               One stage each: the keys' is free while the weights are made,
+//               the values' while the next scores are.
 //   warps 0..3  one thread a row: scores from TMEM, running maximum and sum,
-//               weights back into TMEM.  Warp 0 also issues the products: it
-//               would wait for them anyway.
+//               weights back into TMEM, in two halves, so that the first half's
+//               products run beside the second half's exponentials.
+//   warp 8      issues the products.
 // TMEM, 256 columns, so that two CTAs share an SM and one's products run beside
-// the other's exponentials: the turned query (fp16, the left operand of the
-// scores), 64 columns of scores, whose first half the weights take over (the
-// left operand of the sum), and the sum itself, which stays until the end.
+// the other's exponentials: the scores (KT columns), whose first half the weights
+// take over (the left operand of the sum), and the sum itself (D columns), which
+// stays until the end.  The turned query (fp16) is a shared-memory operand.
 //
 // Scales: as in oq_cattn.cu the running maximum is taken over score + ev, so
-// the weights carry their page's value exponent; a step's four groups of 16
-// tokens (no page is smaller) have their own.  The accumulator is rescaled only
-// when a row's maximum has grown by more than 2^8.
+// the weights carry their page's value exponent; groups of 16 tokens (no page is
+// smaller) have their own.  The accumulator is rescaled only when a row's maximum
+// has grown by more than 2^8.
 //
 // fp16 queries keep a second term: the turn rounds them to 2^-12, which would
 // show beside an fp16 result, so what the first operand leaves out goes into a
-// second one (shared memory) and the scores take both.
+// second one and the scores take both.  (At D = 128 that operand's 32 KB leave
+// room for 64 keys a step instead of 128.)
 //
 // Every wait is bounded (~1 s); one that gives up records OQ_ERR_TIMEOUT and
 // raises a flag that lets all others return at once, and the CTA still reaches
@@ -38,8 +42,9 @@ namespace {
 
 using namespace cattn;
 
-constexpr int kThreads = 256, kRows = 128;
-constexpr int kTmem = 256, kColQ = 0, kColS = 64, kColO = 128;
+constexpr int kThreads = 288, kRows = 128;
+constexpr int kTmem = 256, kColS = 0, kColO = 128;
+constexpr int kStart = 4;  // units of an item's beginning and end
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -118,12 +123,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 template <int N>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b) {  // accumulates
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, 1, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc<N>())
+      "l"(a), "l"(b), "r"(idesc<N>()), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -196,22 +201,25 @@ __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsig
   return r;
 }
 
-// A row's weights 2^(score + ev - top) of 64 keys from its scores in TMEM, as
-// fp16 pairs; `part`: their sums in groups of 16 keys; `mx`: the largest exponent.
-// MASKED: only the first `left` keys are seen.
-template <bool MASKED>
-__device__ __forceinline__ void weigh(uint32_t scores, const float4 (&sc)[4], float fac, float top, int left,
-                                      uint32_t (&p)[32], float (&part)[4], float& mx) {
+// A row's weights 2^(score + ev - top) of KEYS keys from its scores in TMEM, as
+// fp16 pairs, and into `sum` their part of the softmax's sum; `mx`: the largest
+// exponent.  sc: (key scale, ev, 2^-ev) of every 16 keys.  MASKED: only the first
+// `left` keys are seen.
+template <int KEYS, bool MASKED>
+__device__ __forceinline__ float weigh(uint32_t scores, const float4* sc, float fac, float top, int left,
+                                       uint32_t (&p)[KEYS / 2], float& mx) {
   mx = -INFINITY;
+  float sum = 0.0f;
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
+  for (int q = 0; q < KEYS / 32; ++q) {
     uint32_t v[32];
-    tmem_ld32(scores + 32 * hf, v);
+    tmem_ld32(scores + 32 * q, v);
     wait_ld();
 #pragma unroll
     for (int gg = 0; gg < 2; ++gg) {
-      const int g = 2 * hf + gg;
-      const float c = sc[g].x * fac, d = sc[g].x != 0.0f ? sc[g].y - top : -INFINITY;  // an empty page's scores go
+      const int g = 2 * q + gg;
+      const float4 s = sc[g];
+      const float c = s.x * fac, d = s.x != 0.0f ? s.y - top : -INFINITY;  // an empty page's scores go
       const unsigned long long c2 = f2_pack(c, c), d2 = f2_pack(d, d);
       unsigned long long add = f2_pack(0.0f, 0.0f);
 #pragma unroll
@@ -229,65 +237,63 @@ __device__ __forceinline__ void weigh(uint32_t scores, const float4 (&sc)[4], fl
       }
       float s0, s1;
       f2_split(add, s0, s1);
-      part[g] = s0 + s1;
+      sum = fmaf(s0 + s1, s.z, sum);
     }
   }
+  return sum;
 }
 
 template <int D, bool TWO>
 struct Smem {
-  static constexpr int kK = 2 * D * kTile;  // bytes of a stage of keys, and of values
-  static constexpr int kKeys = 0, kValues = 2 * kK;
-  static constexpr int kLow = 4 * kK;       // the query's second term
-  static constexpr int kRowStage = kLow + (TWO ? kRows * D * 2 : 0);      // 16-bit rows being turned
-  static constexpr int kScales = kRowStage + kThreads / (D / 8) * D * 2;  // [4][4] (key scale, ev, 2^-ev)
-  static constexpr int kFac = kScales + 4 * 4 * 16;                       // [rows] factor, limit
-  static constexpr int kStat = kFac + kRows * 8;                          // [rows] maximum, sum
+  static constexpr int KT = TWO && D == 128 ? 64 : 128;  // keys of a step
+  static constexpr int kOperand = 2 * D * KT;            // bytes of the keys, and of the values
+  static constexpr int kKeys = 0, kValues = kOperand, kQuery = 2 * kOperand;
+  static constexpr int kLow = kQuery + kRows * D * 2;    // the query's second term
+  static constexpr int kRowStage = kLow + (TWO ? kRows * D * 2 : 0);        // 16-bit rows being turned
+  static constexpr int kScales = kRowStage + 256 / (D / 8) * D * 2;         // [2][KT / 16] (key scale, ev, 2^-ev)
+  static constexpr int kFac = kScales + 2 * (KT / 16) * 16;                 // [rows] factor, limit
+  static constexpr int kStat = kFac + kRows * 8;                            // [rows] maximum, sum
   static constexpr int kBars = kStat + kRows * 8;
   static constexpr int kTotal = kBars + 128;
   static constexpr int kAlloc = kTotal + 1024;  // room to align the base
-  // aliases of the stages, outside the steps
-  static constexpr int kQStride = D + 8;  // the query rows as fp16, before they go to TMEM
-  static_assert(kRows * kQStride * 2 <= kLow && kRows * D * 4 <= kLow, "what stands in the stages' place");
-  static_assert(2 * (kAlloc + 1024) <= 228 * 1024, "two CTAs an SM");
+  static_assert(kRows * D * 4 <= kRowStage, "the rows' sums stand in the operands' place at the end");
+  static_assert(2 * (kAlloc + 2048) <= 228 * 1024, "two CTAs an SM");
 };
 
 template <typename T, int D, bool TWO>
 __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constant__ Args a) {
   using S = Smem<D, TWO>;
-  constexpr int LPR = D / 8;
+  constexpr int KT = S::KT, HK = KT / 2, LPR = D / 8;
   extern __shared__ unsigned char sm_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* row_fac = reinterpret_cast<float*>(sm + S::kFac);
   int* row_lim = reinterpret_cast<int*>(sm + S::kFac) + kRows;
   float2* row_stat = reinterpret_cast<float2*>(sm + S::kStat);
   float4* scales = reinterpret_cast<float4*>(sm + S::kScales);
-  __half* qs = reinterpret_cast<__half*>(sm);
   const uint32_t bars = base + S::kBars;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + S::kBars + 104);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 112);
   auto bar = [&](int i) { return bars + 8u * i; };
-  constexpr int K_FULL = 0, K_EMPTY = 2, V_FULL = 4, V_EMPTY = 6, S_FULL = 8, P_FULL = 9, O_FULL = 10;
+  constexpr int K_FULL = 0, K_EMPTY = 1, V_FULL = 2, V_EMPTY = 3, S_FULL = 4, P_FULL = 5, HALF = 7, O_FULL = 8;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(K_FULL + i), 4), mbar_init(bar(K_EMPTY + i), 1);
-      mbar_init(bar(V_FULL + i), 4), mbar_init(bar(V_EMPTY + i), 1);
-    }
-    mbar_init(bar(S_FULL), 1), mbar_init(bar(P_FULL), 4), mbar_init(bar(O_FULL), 1);
+    mbar_init(bar(K_FULL), 4), mbar_init(bar(K_EMPTY), 1);
+    mbar_init(bar(V_FULL), 4), mbar_init(bar(V_EMPTY), 1);
+    mbar_init(bar(S_FULL), 1), mbar_init(bar(P_FULL), 4), mbar_init(bar(P_FULL + 1), 4);
+    mbar_init(bar(HALF), 1), mbar_init(bar(O_FULL), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 4) {
+  if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                  "r"(kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   const int cta = blockIdx.x;
-  const Share sh = find_share<kRows, kThreads>(a, cta, gridDim.x);
+  const Share sh = find_share<kRows, KT, kStart, kThreads>(a, cta, gridDim.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -307,99 +313,92 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
 
   while (at < stop && b < a.B) {
     const Seq s = load_seq(a, b, false);
-    const long long per_head = head_work<kRows>(a, s);
+    const long long per_head = units_before<kRows, KT, kStart>(a, s, row_tiles<kRows>(s));
     if (into >= per_head * a.c.heads) {
       ++b;
       into = 0;
       continue;
     }
-    const int h = (int)(into / per_head);
-    long long rem = into - h * per_head;
-    int qt = 0, work = tile_work<kRows>(a, s, 0);
-    while (rem >= work) {
-      rem -= work;
-      work = tile_work<kRows>(a, s, ++qt);
+    const Part part = find_part<kRows, KT, kStart>(a, s, per_head, into, stop - at);
+    const int h = part.h, qt = part.qt, keys = part.keys, t0 = part.t0, take = part.t1 - part.t0;
+    const bool first = t0 == 0, last = part.t1 == part.tiles;
+    const size_t slot = ((size_t)2 * cta + (first ? 1 : 0)) * kRows;
+    const long long item_end = at - into + part.end;
+    at += part.units;
+    into += part.units;
+    if (take == 0) {  // no key tile: nothing to do, but a piece that the join counts on says so
+      if (t0 > 0 && tid < kRows) *reinterpret_cast<float2*>(a.stat + 2 * (slot + tid)) = make_float2(-INFINITY, 0.0f);
+      continue;
     }
-    const int t0 = (int)rem, take = (int)min((long long)(work - t0), stop - at);
-    const int keys = tile_keys<kRows>(a, s, qt);
     const int rows = min(kRows, s.rows - qt * kRows);
+    const int tok0 = t0 * KT;
 
-    // the item's query rows: turned, scaled by a power of two, fp16
-    constexpr int PASS = kThreads / LPR, BATCH = 4;
-    for (int p = 0; p < kRows; p += BATCH * PASS) {
-      uint4 w[BATCH];
+    // the item's query rows: turned, scaled by a power of two, fp16, as an operand
+    constexpr int PASS = 256 / LPR, BATCH = 4;
+    if (warp < 8) {
+      for (int p = 0; p < kRows; p += BATCH * PASS) {
+        uint4 w[BATCH];
+        int token[BATCH];
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int r = p + k * PASS + tid / LPR, gr = qt * kRows + r, i = gr / a.group;
-        w[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows)
-          w[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + i) * a.qt +
-                                                 ((long long)h * a.group + (gr - i * a.group)) * a.qh + 8 * l);
+        for (int k = 0; k < BATCH; ++k) {
+          const int r = p + k * PASS + tid / LPR, gr = qt * kRows + r;
+          token[k] = row_token(a, gr);
+          w[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows)
+            w[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + token[k]) * a.qt +
+                                                   ((long long)h * a.group + (gr - token[k] * a.group)) * a.qh + 8 * l);
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const int r = p + k * PASS + tid / LPR;
+          float x[8];
+          if (a.r.perm) {
+            *reinterpret_cast<uint4*>(stage_row + 8 * l) = w[k];
+            __syncwarp();
+            rotate_row<T>(stage_row, turn, l, a.r, x);
+            __syncwarp();
+          } else {
+            unpack8<T>(w[k], x);
+          }
+          float top = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+          for (int m = LPR / 2; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+          const int e = min(max(scale_exp(top), -100), 120);
+          const float f = pow2(-e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] *= f;
+          const uint4 hi = pack8<__half>(x);
+          const uint32_t to = (uint32_t)((l >> 3) * (kRows * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4));
+          sts128(base + S::kQuery + to, hi.x, hi.y, hi.z, hi.w);
+          if constexpr (TWO) {
+            float y[8];
+            unpack8<__half>(hi, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = x[j] - y[j];
+            const uint4 lo = pack8<__half>(y);
+            sts128(base + S::kLow + to, lo.x, lo.y, lo.z, lo.w);
+          }
+          if (l == 0) {
+            row_fac[r] = pow2(e) * a.scale;
+            // a row that is not there is not masked, and not used
+            row_lim[r] = r >= rows ? 0x7FFFFFFF : a.causal ? s.len - s.n + token[k] + 1 : s.len;
+          }
+        }
       }
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int r = p + k * PASS + tid / LPR, i = (qt * kRows + r) / a.group;
-        float x[8];
-        if (a.r.perm) {
-          *reinterpret_cast<uint4*>(stage_row + 8 * l) = w[k];
-          __syncwarp();
-          rotate_row<T>(stage_row, turn, l, a.r, x);
-          __syncwarp();
-        } else {
-          unpack8<T>(w[k], x);
-        }
-        float top = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-#pragma unroll
-        for (int m = LPR / 2; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-        const int e = min(max(scale_exp(top), -100), 120);
-        const float f = pow2(-e);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= f;
-        const uint4 hi = pack8<__half>(x);
-        *reinterpret_cast<uint4*>(qs + r * S::kQStride + 8 * l) = hi;
-        if constexpr (TWO) {
-          float y[8];
-          unpack8<__half>(hi, y);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = x[j] - y[j];
-          const uint4 lo = pack8<__half>(y);
-          sts128(base + S::kLow + (l >> 3) * (kRows * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
-        }
-        if (l == 0) {
-          row_fac[r] = pow2(e) * a.scale;
-          row_lim[r] = r >= rows ? 0x7FFFFFFF : a.causal ? s.len - s.n + i + 1 : s.len;  // no row: not masked, not used
-        }
-      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if constexpr (TWO) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    if (warp < 4) {
-      const uint4* q = reinterpret_cast<const uint4*>(qs + tid * S::kQStride);
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t v[32];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 w = q[8 * c + j];
-          v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
-        }
-        tmem_st32(tmem_row + kColQ + 32 * c, v);
-      }
-      wait_st();
-    }
-    tc_fence_before();
-    __syncthreads();  // the query stands in TMEM, its staging may be written over
-    tc_fence_after();
 
-    const int tok0 = t0 * kTile;
-    if (warp >= 4) {
+    if (warp >= 4 && warp < 8) {
       // ---- expanding the codes ----
+      constexpr int NH = KT / 64;           // pieces of 64 keys
       const int ct = tid - 128;
-      const int kn = ct & 63, kh = ct >> 6;           // a token's row, which half of it
-      const int vc = ct & 7, vg = ct >> 3;            // eight tokens, D / 16 coordinates
-      constexpr int KW = D / 32;                      // 16-byte vectors of codes of half a row
-      constexpr int VW = D / 64;                      // words of D / 16 codes
+      const int kn = ct & 63, kh = ct >> 6;  // a token's row, which half of it
+      const int vc = ct & 7, vg = ct >> 3;   // eight tokens, D / 16 coordinates
+      constexpr int KW = D / 32;             // 16-byte vectors of codes of half a row
+      constexpr int VW = D / 64;             // words of D / 16 codes
       const int* table = a.table + (size_t)b * a.width;
       auto row_at = [&](int tok) -> size_t {  // row of codes of a token (some row where there is none)
         int page = 0;
@@ -409,196 +408,207 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
         }
         return (((size_t)page * a.c.heads + h) << plog) + (tok & (a.c.page - 1));
       };
-      uint4 kw[KW];
-      uint32_t vw[8][VW];
-      auto load_k = [&](int t) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.c.k + row_at(tok0 + t * kTile + kn) * D + kh * (D / 2));
+      uint32_t code[NH][D / 8];  // of the keys' piece or the values', whichever comes next
+      auto load_k = [&](int t, int i) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.c.k + row_at(tok0 + t * KT + 64 * i + kn) * D + kh * (D / 2));
 #pragma unroll
-        for (int j = 0; j < KW; ++j) kw[j] = p[j];
+        for (int j = 0; j < KW; ++j) {
+          const uint4 w = p[j];
+          code[i][4 * j] = w.x, code[i][4 * j + 1] = w.y, code[i][4 * j + 2] = w.z, code[i][4 * j + 3] = w.w;
+        }
       };
-      auto load_v = [&](int t) {
-        const int8_t* p = a.c.v + row_at(tok0 + t * kTile + 8 * vc) * D + vg * (D / 16);
+      auto load_v = [&](int t, int i) {
+        const int8_t* p = a.c.v + row_at(tok0 + t * KT + 64 * i + 8 * vc) * D + vg * (D / 16);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if constexpr (VW == 2) {
             const uint2 w = *reinterpret_cast<const uint2*>(p + j * D);
-            vw[j][0] = w.x, vw[j][1] = w.y;
+            code[i][2 * j] = w.x, code[i][2 * j + 1] = w.y;
           } else {
-            vw[j][0] = *reinterpret_cast<const uint32_t*>(p + j * D);
+            code[i][j] = *reinterpret_cast<const uint32_t*>(p + j * D);
           }
         }
       };
-      float4 sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
-      auto load_scales = [&](int t) {  // four threads, a group of 16 tokens each
-        const int tok = tok0 + t * kTile + 16 * ct;
-        sc = make_float4(0.0f, 0.0f, 1.0f, 0.0f);  // a key scale of 0: no keys
+      float2 sc = make_float2(0.0f, 1.0f);
+      auto load_scales = [&](int t) {  // a thread for each group of 16 tokens
+        const int tok = tok0 + t * KT + 16 * ct;
+        sc = make_float2(0.0f, 1.0f);  // a key scale of 0: no keys
         if (tok < keys) {
           const int page = table[tok >> plog];
           if (page >= 0 && page < a.c.n_pages) {
             const size_t ph = (size_t)page * a.c.heads + h;
-            sc.x = a.c.ks[ph], sc.y = a.c.vs[ph];
+            sc = make_float2(a.c.ks[ph], a.c.vs[ph]);
           } else {
             bad_index(a.status);
           }
         }
       };
-      load_k(0);
-      load_v(0);
-      if (ct < 4) load_scales(0);
+#pragma unroll
+      for (int i = 0; i < NH; ++i) load_k(0, i);
+      if (ct < KT / 16) load_scales(0);
       for (int t = 0; t < take; ++t) {
-        const uint32_t it = steps + t, st = it & 1u, ph = (it >> 1) & 1u;
-        wait_bounded(bar(K_EMPTY + st), ph ^ 1u, abort_flag, a.status);
+        const uint32_t it = steps + t, ph = it & 1u;
+        wait_bounded(bar(K_EMPTY), ph ^ 1u, abort_flag, a.status);
         __syncwarp();
-        const uint32_t kb = base + S::kKeys + st * S::kK;
 #pragma unroll
-        for (int j = 0; j < KW; ++j) {
-          const uint32_t w[4] = {kw[j].x ^ 0x80808080u, kw[j].y ^ 0x80808080u, kw[j].z ^ 0x80808080u,
-                                 kw[j].w ^ 0x80808080u};
+        for (int i = 0; i < NH; ++i) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {  // eight codes: one 16-byte chunk of the row's 128-byte blocks
-            const int chunk = kh * (D / 16) + 2 * j + u;
-            sts128(kb + (chunk >> 3) * (kTile * 128) + kn * 128 + (((chunk & 7) ^ (kn & 7)) << 4),
-                   bytes2(w[2 * u], 0x4140), bytes2(w[2 * u], 0x4342), bytes2(w[2 * u + 1], 0x4140),
-                   bytes2(w[2 * u + 1], 0x4342));
+          for (int j = 0; j < KW; ++j) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // eight codes: one 16-byte chunk of the row's 128-byte blocks
+              const uint32_t w0 = code[i][4 * j + 2 * u] ^ 0x80808080u, w1 = code[i][4 * j + 2 * u + 1] ^ 0x80808080u;
+              const int chunk = kh * (D / 16) + 2 * j + u;
+              sts128(base + S::kKeys + (chunk >> 3) * (KT * 128) + (64 * i + kn) * 128 + (((chunk & 7) ^ (kn & 7)) << 4),
+                     bytes2(w0, 0x4140), bytes2(w0, 0x4342), bytes2(w1, 0x4140), bytes2(w1, 0x4342));
+            }
           }
+          load_v(t, i);
         }
-        if (ct < 4) {
+        if (ct < KT / 16) {
           const int ev = min(max(scale_exp(sc.y), -126), 126);
-          scales[(it & 3u) * 4 + ct] = make_float4(sc.x, (float)ev, pow2(-ev), 0.0f);
+          scales[ph * (KT / 16) + ct] = make_float4(sc.x, (float)ev, pow2(-ev), 0.0f);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(K_FULL + st));
-        if (t + 1 < take) {
-          load_k(t + 1);
-          if (ct < 4) load_scales(t + 1);
-        }
+        if (lane == 0) mbar_arrive(bar(K_FULL));
+        if (t + 1 < take && ct < KT / 16) load_scales(t + 1);
 
-        wait_bounded(bar(V_EMPTY + st), ph ^ 1u, abort_flag, a.status);
+        wait_bounded(bar(V_EMPTY), ph ^ 1u, abort_flag, a.status);
         __syncwarp();
-        const uint32_t vb = base + S::kValues + st * S::kK;
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          uint32_t o[4][4];  // [coordinate][pair of tokens]
+        for (int i = 0; i < NH; ++i) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t x0 = vw[2 * q][w] ^ 0x80808080u, x1 = vw[2 * q + 1][w] ^ 0x80808080u;
-            const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
-            o[0][q] = bytes2(lo, 0x4140), o[1][q] = bytes2(lo, 0x4342);
-            o[2][q] = bytes2(hi, 0x4140), o[3][q] = bytes2(hi, 0x4342);
+          for (int w = 0; w < VW; ++w) {
+            uint32_t o[4][4];  // [coordinate][pair of tokens]
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t x0 = code[i][VW * (2 * q) + w] ^ 0x80808080u, x1 = code[i][VW * (2 * q + 1) + w] ^ 0x80808080u;
+              const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
+              o[0][q] = bytes2(lo, 0x4140), o[1][q] = bytes2(lo, 0x4342);
+              o[2][q] = bytes2(hi, 0x4140), o[3][q] = bytes2(hi, 0x4342);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int d = vg * (D / 16) + 4 * w + k;
+              sts128(base + S::kValues + i * (D * 128) + d * 128 + ((vc ^ (d & 7)) << 4), o[k][0], o[k][1], o[k][2], o[k][3]);
+            }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int d = vg * (D / 16) + 4 * w + i;
-            sts128(vb + d * 128 + ((vc ^ (d & 7)) << 4), o[i][0], o[i][1], o[i][2], o[i][3]);
-          }
+          if (t + 1 < take) load_k(t + 1, i);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(V_FULL + st));
-        if (t + 1 < take) load_v(t + 1);
+        if (lane == 0) mbar_arrive(bar(V_FULL));
       }
-    } else {
-      // ---- scores, weights, products ----
-      auto scores = [&](uint32_t it) {  // warp 0
-        const uint32_t st = it & 1u;
-        wait_bounded(bar(K_FULL + st), (it >> 1) & 1u, abort_flag, a.status);
+    } else if (warp == 8) {
+      // ---- products ----
+      const uint64_t qd = desc_sw128(base + S::kQuery), ld = desc_sw128(base + S::kLow);
+      const uint64_t kd = desc_sw128(base + S::kKeys), vd = desc_sw128(base + S::kValues);
+      for (int t = 0; t < take; ++t) {
+        const uint32_t ph = (steps + t) & 1u;
+        wait_bounded(bar(K_FULL), ph, abort_flag, a.status);
         __syncwarp();
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t kd = desc_sw128(base + S::kKeys + st * S::kK);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ts<kTile>(tmem + kColS, tmem + kColQ + 8 * k, kd + (uint64_t)((k >> 2) * (kTile * 128 / 16) + (k & 3) * 2),
-                          k > 0);
+            mma_ss<KT>(tmem + kColS, qd + (uint64_t)((k >> 2) * (kRows * 8) + (k & 3) * 2),
+                       kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), k > 0);
           if constexpr (TWO) {
-            const uint64_t ld = desc_sw128(base + S::kLow);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              mma_ss<kTile>(tmem + kColS, ld + (uint64_t)((k >> 2) * (kRows * 128 / 16) + (k & 3) * 2),
-                            kd + (uint64_t)((k >> 2) * (kTile * 128 / 16) + (k & 3) * 2));
+              mma_ss<KT>(tmem + kColS, ld + (uint64_t)((k >> 2) * (kRows * 8) + (k & 3) * 2),
+                         kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), 1u);
           }
-          commit(bar(K_EMPTY + st));
+          commit(bar(K_EMPTY));
           commit(bar(S_FULL));
         }
         __syncwarp();
-      };
-      if (warp == 0) scores(steps);
+        wait_bounded(bar(V_FULL), ph, abort_flag, a.status);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          wait_bounded(bar(P_FULL + hf), ph, abort_flag, a.status);
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = hf * (HK / 16); k < (hf + 1) * (HK / 16); ++k)
+              mma_ts<D>(tmem + kColO, tmem + kColS + 8 * k, vd + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), t > 0 || k > 0);
+            if (hf == 0) {
+              commit(bar(HALF));
+            } else {
+              commit(bar(V_EMPTY));
+              if (t + 1 == take) commit(bar(O_FULL));
+            }
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp < 4) {
+      // ---- weights ----
       const float fac = row_fac[tid];
       const int lim = row_lim[tid];
       float top = 0.0f, sum = 0.0f;
       bool none = true;  // no key seen so far: the maximum says nothing
       for (int t = 0; t < take; ++t) {
-        const uint32_t it = steps + t;
-        const int tok = tok0 + t * kTile;
-        wait_bounded(bar(S_FULL), it & 1u, abort_flag, a.status);
+        const uint32_t it = steps + t, ph = it & 1u;
+        wait_bounded(bar(S_FULL), ph, abort_flag, a.status);
         __syncwarp();
         tc_fence_after();
-        float4 sc[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) sc[g] = scales[(it & 3u) * 4 + g];
-        // The weights at once, against the maximum so far; in the rare step that
-        // raises it (2^8 and more above, or the first keys of a row) once more
-        // from the scores, which still stand in TMEM.
-        uint32_t p[32];
-        const int left = lim - tok;  // keys of the step that the row may see
-        const bool whole = __all_sync(0xFFFFFFFFu, left >= kTile);
-        for (int tries = 0; tries < 2; ++tries) {
-          float mx, part[4];
-          if (whole)
-            weigh<false>(tmem_row + kColS, sc, fac, top, left, p, part, mx);
-          else
-            weigh<true>(tmem_row + kColS, sc, fac, top, left, p, part, mx);
-          const bool raise = mx > 8.0f || (none && mx > -INFINITY);
-          if (tries > 0 || !__any_sync(0xFFFFFFFFu, raise)) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) sum = fmaf(part[g], sc[g].z, sum);
-            break;
-          }
-          const float up = raise ? mx : 0.0f;
-          const float f = none ? 1.0f : ex2(-up);  // nothing to rescale before the first key
-          top += up;
-          if (raise) none = false;
-          sum *= f;
-          if (t > 0) {  // the sum so far stands in TMEM, and no product is under way
+        for (int hf = 0; hf < 2; ++hf) {
+          const float4* sc = scales + ph * (KT / 16) + hf * (HK / 16);
+          const uint32_t from = tmem_row + kColS + HK * hf;
+          const int left = lim - (tok0 + t * KT + HK * hf);  // keys of the half that the row may see
+          const bool whole = __all_sync(0xFFFFFFFFu, left >= HK);
+          // The weights at once, against the maximum so far; in the rare step that
+          // raises it (2^8 and more above, or the first keys of a row) once more
+          // from the scores, which still stand in TMEM.
+          uint32_t p[HK / 2];
+          for (int tries = 0; tries < 2; ++tries) {
+            float mx;
+            const float more = whole ? weigh<HK, false>(from, sc, fac, top, left, p, mx)
+                                     : weigh<HK, true>(from, sc, fac, top, left, p, mx);
+            const bool raise = mx > 8.0f || (none && mx > -INFINITY);
+            if (tries > 0 || !__any_sync(0xFFFFFFFFu, raise)) {
+              sum += more;
+              break;
+            }
+            const float up = raise ? mx : 0.0f;
+            const float f = none ? 1.0f : ex2(-up);  // nothing to rescale before the first key
+            top += up;
+            if (raise) none = false;
+            sum *= f;
+            if (hf == 1) {  // the first half's products must have been added
+              wait_bounded(bar(HALF), ph, abort_flag, a.status);
+              __syncwarp();
+              tc_fence_after();
+            }
+            if (t > 0 || hf > 0) {  // the sum so far stands in TMEM, and no product is under way
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(tmem_row + kColO + c, o);
-              wait_ld();
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tmem_row + kColO + c, o);
+                wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(tmem_row + kColO + c, o);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(tmem_row + kColO + c, o);
+              }
             }
           }
-        }
-        tmem_st32(tmem_row + kColS, p);
-        wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(P_FULL));
-        if (warp == 0) {
-          const uint32_t st = it & 1u;
-          wait_bounded(bar(P_FULL), it & 1u, abort_flag, a.status);
-          wait_bounded(bar(V_FULL + st), (it >> 1) & 1u, abort_flag, a.status);
+          if constexpr (HK == 64)
+            tmem_st32(tmem_row + kColS + 32 * hf, p);
+          else
+            tmem_st16(tmem_row + kColS + 16 * hf, p);
+          wait_st();
+          tc_fence_before();
           __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t vd = desc_sw128(base + S::kValues + st * S::kK);
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts<D>(tmem + kColO, tmem + kColS + 8 * k, vd + (uint64_t)(2 * k), t > 0 || k > 0);
-            commit(bar(V_EMPTY + st));
-            if (t + 1 == take) commit(bar(O_FULL));
-          }
-          __syncwarp();
-          if (t + 1 < take) scores(it + 1);
+          if (lane == 0) mbar_arrive(bar(P_FULL + hf));
         }
       }
       wait_bounded(bar(O_FULL), items & 1u, abort_flag, a.status);
       __syncwarp();
       tc_fence_after();
-      // the rows' sums into shared memory (the stages' place), 16-byte chunks turned by the row
+      // the rows' sums into shared memory (the operands' place), 16-byte chunks turned by the row
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -608,72 +618,72 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
         for (int j = 0; j < 8; ++j)
           sts128(base + tid * (D * 4) + (((c / 4 + j) ^ (tid & 7)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
       }
-      row_stat[tid] = make_float2(none ? -INFINITY : top, sum);
+      row_stat[tid] = make_float2(none && sum == sum ? -INFINITY : top, sum);  // (a NaN query's piece counts)
       tc_fence_before();
     }
     __syncthreads();
-    const bool first = t0 == 0, last = t0 + take == work;
-    const size_t slot = ((size_t)2 * cta + (first ? 1 : 0)) * kRows;
+    if (warp < 8) {
 #pragma unroll 2
-    for (int p = 0; p < kRows; p += PASS) {
-      const int r = p + tid / LPR;
-      const float4 lo = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l) ^ (r & 7)) << 4));
-      const float4 hi = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l + 1) ^ (r & 7)) << 4));
-      float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      const float2 stat = row_stat[r];
-      if (first && last) {
-        const float inv = stat.y > 0.0f ? 1.0f / stat.y : stat.y == 0.0f ? 0.0f : stat.y;
+      for (int p = 0; p < kRows; p += PASS) {
+        const int r = p + tid / LPR;
+        const float4 lo = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l) ^ (r & 7)) << 4));
+        const float4 hi = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l + 1) ^ (r & 7)) << 4));
+        float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const float2 stat = row_stat[r];
+        if (first && last) {
+          const float inv = stat.y > 0.0f ? 1.0f / stat.y : stat.y == 0.0f ? 0.0f : stat.y;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= inv;
-        uint4 w;
-        if (a.r.perm) {
-          unrotate_row<T>(x, turn, l, a.r, stage_row);
-          __syncwarp();
-          w = *reinterpret_cast<const uint4*>(stage_row + 8 * l);
-          __syncwarp();
-        } else {
-          w = pack8<T>(x);
+          for (int k = 0; k < 8; ++k) x[k] *= inv;
+          uint4 w;
+          if (a.r.perm) {
+            unrotate_row<T>(x, turn, l, a.r, stage_row);
+            __syncwarp();
+            w = *reinterpret_cast<const uint4*>(stage_row + 8 * l);
+            __syncwarp();
+          } else {
+            w = pack8<T>(x);
+          }
+          const int gr = qt * kRows + r, i = row_token(a, gr);
+          if (r < rows)
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
+                                      ((long long)h * a.group + (gr - i * a.group)) * a.oh + 8 * l) = w;
+        } else if (r < rows) {
+          float4* o = reinterpret_cast<float4*>(a.piece + (slot + r) * D + 8 * l);
+          o[0] = lo, o[1] = hi;
+          if (l == 0) *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = stat;
         }
-        const int gr = qt * kRows + r, i = gr / a.group;
-        if (r < rows)
-          *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
-                                    ((long long)h * a.group + (gr - i * a.group)) * a.oh + 8 * l) = w;
-      } else if (r < rows) {
-        float4* o = reinterpret_cast<float4*>(a.piece + (slot + r) * D + 8 * l);
-        o[0] = lo, o[1] = hi;
-        if (l == 0) *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = stat;
       }
     }
-    if (first && !last) desc = make_int4((int)((at - t0 + work - 1) / sh.size) - cta + 1, b, h, qt);
+    if (first && !last) desc = make_int4((int)((item_end - 1) / sh.size) - cta + 1, b, h, qt);
     __syncthreads();
     steps += take;
     ++items;
-    at += take;
-    into += take;
   }
   if (tid == 0) a.desc[cta] = desc;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4)
+  if (warp == 8)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
 }
 
 template <typename T, int D, bool TWO>
 int launch(const Args& a, cudaStream_t s) {
+  using S = Smem<D, TWO>;
   auto kern = chunk_kernel<T, D, TWO>;
-  const int smem = Smem<D, TWO>::kAlloc;
   int per_sm = 0, nsm = 0;
-  if (int rc = occupancy(reinterpret_cast<const void*>(kern), smem, kThreads, 0, &per_sm)) return rc;
+  // (raises the kernel's shared-memory limit; the query itself says one CTA an SM
+  // for a kernel that allocates TMEM, where two share its registers, shared memory
+  // and TMEM by construction; none waits for another)
+  if (int rc = occupancy(reinterpret_cast<const void*>(kern), S::kAlloc, kThreads, 0, &per_sm)) return rc;
   if (int rc = sm_count(&nsm)) return rc;
   if (per_sm < 1) return fail(OQ_ERR_UNSUPPORTED, "attention kernel does not fit");
-  // two CTAs share an SM's registers, shared memory and TMEM by construction (the
-  // occupancy query says one for a kernel that allocates TMEM); none waits for another
+  // no more CTAs than units that there can be
   const long long rows = (long long)a.T * a.group;
   const long long items = std::min<long long>((rows + kRows - 1) / kRows + a.B, rows) * a.c.heads;
-  const long long tiles = items * std::max<long long>(1, ((long long)a.width * a.c.page + kTile - 1) / kTile);
-  const int ctas = (int)std::min<long long>(tiles, std::min(2 * nsm, kChunkCtas));
-  kern<<<ctas, kThreads, smem, s>>>(a);
+  const long long units = items * (kStart + 1 + (long long)a.width * a.c.page / S::KT);
+  const int ctas = (int)std::min<long long>(units, std::min(2 * nsm, kChunkCtas));
+  kern<<<ctas, kThreads, S::kAlloc, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   join_kernel<T, D, kRows><<<dim3((unsigned)ctas, 16), 128, 0, s>>>(a, 0);

@@ -435,8 +435,8 @@ struct Plan {
 Plan plan_of(int T, int B, int group) {
   Plan p;
   const long long per = ((long long)T * group + B - 1) / std::max(1, B);  // rows of a sequence, on average
-  p.rows = per <= 8 ? 8 : per <= 16 ? 16 : 128;
-  p.ctas = p.rows == 128 ? kChunkCtas : kStepCtas;
+  p.rows = per <= 8 ? 8 : per <= 16 ? 16 : 256;
+  p.ctas = p.rows == 256 ? kChunkCtas : kStepCtas;
   return p;
 }
 
@@ -492,7 +492,7 @@ int launch_cattn(const AttnCall& c) {
   a.piece = static_cast<float*>(c.workspace);
   a.stat = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d));
   a.desc = reinterpret_cast<int4*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d) + stat_bytes(p));
-  if (p.rows == 128) return launch_cattn_chunk(a, c.dtype, v->d, c.stream);
+  if (p.rows == 256) return launch_cattn_chunk(a, c.dtype, v->d, c.stream);
   cudaStream_t s = (cudaStream_t)c.stream;
 #define OQ_STEP(T, D, TWO) \
   return p.rows == 8 ? launch_step<T, D, 1, TWO>(a, p.ctas, s) : launch_step<T, D, 2, TWO>(a, p.ctas, s)

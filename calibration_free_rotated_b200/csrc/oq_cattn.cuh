@@ -29,7 +29,7 @@ namespace cattn {
 using namespace cache;
 
 // Most CTAs that the workspace has pieces for (the kernels' residency on 148 SMs).
-constexpr int kStepCtas = 148 * 4, kChunkCtas = 148 * 2;
+constexpr int kStepCtas = 148 * 4, kChunkCtas = 148;
 
 struct Args {
   View c;

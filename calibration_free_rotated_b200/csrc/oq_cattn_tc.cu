@@ -1,22 +1,22 @@
 // Attention over the 8-bit cache for many query rows (chunks of new tokens,
 // whole images): bound by the tensor cores and what feeds them.
 //
-// The same sums as oq_cattn.cu, on tcgen05: a CTA takes 128 query rows and walks
-// KT keys a step.  Three roles:
-//   warps 4..7  expand the step's codes to fp16 (exact) into the K-major
-//               128-byte-swizzled layout of the tensor cores' operands, the keys
-//               as they lie, the values transposed by byte permutes, 64 keys at
-//               a time with the codes of what comes next already in registers.
-//               One stage each: the keys' is free while the weights are made,
-//               the values' while the next scores are.
-//   warps 0..3  one thread a row: scores from TMEM, running maximum and sum,
-//               weights back into TMEM, in two halves, so that the first half's
-//               products run beside the second half's exponentials.
-//   warp 8      issues the products.
-// TMEM, 256 columns, so that two CTAs share an SM and one's products run beside
-// the other's exponentials: the scores (KT columns), whose first half the weights
-// take over (the left operand of the sum), and the sum itself (D columns), which
-// stays until the end.  The turned query (fp16) is a shared-memory operand.
+// The same sums as oq_cattn.cu, on tcgen05: a CTA (one on each SM) takes 256 query
+// rows as two tiles of 128 and walks KT keys a step.  Three roles:
+//   warps 8..11  expand the step's codes to fp16 (exact) into the K-major
+//                128-byte-swizzled layout of the tensor cores' operands, once for
+//                both tiles: the keys as they lie, the values transposed by byte
+//                permutes, with the codes of what comes next already in registers.
+//   warps 0..7   four a tile, one thread a row: scores from TMEM, running maximum
+//                and sum, weights back into TMEM in two halves, so that the first
+//                half's products run beside the second half's exponentials.
+//   warp 12      issues the products; one tile's run beside the other tile's
+//                exponentials.
+// TMEM, all 512 columns: each tile's scores (KT columns), whose first half the
+// weights take over (the left operand of the sum), and each tile's sum (D
+// columns), which stays until the end.  The turned queries (fp16) are
+// shared-memory operands.  (Two CTAs an SM of one tile each, which expand the
+// codes twice, took 1.9 times as long: issue slots and the level-1 cache.)
 //
 // Scales: as in oq_cattn.cu the running maximum is taken over score + ev, so
 // the weights carry their page's value exponent; groups of 16 tokens (no page is
@@ -42,8 +42,8 @@ namespace {
 
 using namespace cattn;
 
-constexpr int kThreads = 288, kRows = 128;
-constexpr int kTmem = 256, kColS = 0, kColO = 128;
+constexpr int kThreads = 416, kRows = 256, kTileRows = 128;
+constexpr int kTmem = 512, kColS = 0, kColO = 256;  // a tile's columns begin 128 further on
 constexpr int kStart = 4;  // units of an item's beginning and end
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
@@ -245,25 +245,27 @@ __device__ __forceinline__ float weigh(uint32_t scores, const float4* sc, float 
 
 template <int D, bool TWO>
 struct Smem {
-  static constexpr int KT = TWO && D == 128 ? 64 : 128;  // keys of a step
-  static constexpr int kOperand = 2 * D * KT;            // bytes of the keys, and of the values
-  static constexpr int kKeys = 0, kValues = kOperand, kQuery = 2 * kOperand;
-  static constexpr int kLow = kQuery + kRows * D * 2;    // the query's second term
-  static constexpr int kRowStage = kLow + (TWO ? kRows * D * 2 : 0);        // 16-bit rows being turned
+  static constexpr int KT = 128;                             // keys of a step
+  static constexpr int VST = TWO && D == 128 ? 1 : 2;        // stages of values
+  static constexpr int kOperand = 2 * D * KT;                // bytes of a stage of keys, of values
+  static constexpr int kTileQ = kTileRows * D * 2;           // of a tile's queries
+  static constexpr int kKeys = 0, kValues = kOperand, kQuery = (1 + VST) * kOperand;
+  static constexpr int kLow = kQuery + 2 * kTileQ;           // the queries' second term
+  static constexpr int kRowStage = kLow + (TWO ? 2 * kTileQ : 0);           // 16-bit rows being turned
   static constexpr int kScales = kRowStage + 256 / (D / 8) * D * 2;         // [2][KT / 16] (key scale, ev, 2^-ev)
   static constexpr int kFac = kScales + 2 * (KT / 16) * 16;                 // [rows] factor, limit
   static constexpr int kStat = kFac + kRows * 8;                            // [rows] maximum, sum
   static constexpr int kBars = kStat + kRows * 8;
-  static constexpr int kTotal = kBars + 128;
+  static constexpr int kTotal = kBars + 192;
   static constexpr int kAlloc = kTotal + 1024;  // room to align the base
   static_assert(kRows * D * 4 <= kRowStage, "the rows' sums stand in the operands' place at the end");
-  static_assert(2 * (kAlloc + 2048) <= 228 * 1024, "two CTAs an SM");
+  static_assert(kAlloc <= 226 * 1024, "shared memory of a CTA");
 };
 
 template <typename T, int D, bool TWO>
-__global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Args a) {
   using S = Smem<D, TWO>;
-  constexpr int KT = S::KT, HK = KT / 2, LPR = D / 8;
+  constexpr int KT = S::KT, HK = KT / 2, LPR = D / 8, VST = S::VST;
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(sm);
@@ -273,20 +275,23 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
   float2* row_stat = reinterpret_cast<float2*>(sm + S::kStat);
   float4* scales = reinterpret_cast<float4*>(sm + S::kScales);
   const uint32_t bars = base + S::kBars;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + S::kBars + 104);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 112);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + S::kBars + 176);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 180);
   auto bar = [&](int i) { return bars + 8u * i; };
-  constexpr int K_FULL = 0, K_EMPTY = 1, V_FULL = 2, V_EMPTY = 3, S_FULL = 4, P_FULL = 5, HALF = 7, O_FULL = 8;
+  // of the two tiles (S_FULL + w) and of a tile's halves (P_FULL + 2 w + half)
+  constexpr int K_FULL = 0, K_EMPTY = 1, V_FULL = 2, V_EMPTY = 4, S_FULL = 6, P_FULL = 8, HALF = 12, O_FULL = 14;
 
   if (tid == 0) {
     mbar_init(bar(K_FULL), 4), mbar_init(bar(K_EMPTY), 1);
-    mbar_init(bar(V_FULL), 4), mbar_init(bar(V_EMPTY), 1);
-    mbar_init(bar(S_FULL), 1), mbar_init(bar(P_FULL), 4), mbar_init(bar(P_FULL + 1), 4);
-    mbar_init(bar(HALF), 1), mbar_init(bar(O_FULL), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(V_FULL + i), 4), mbar_init(bar(V_EMPTY + i), 1);
+      mbar_init(bar(S_FULL + i), 1), mbar_init(bar(HALF + i), 1), mbar_init(bar(O_FULL + i), 1);
+      mbar_init(bar(P_FULL + 2 * i), 4), mbar_init(bar(P_FULL + 2 * i + 1), 4);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                  "r"(kTmem)
                  : "memory");
@@ -298,16 +303,15 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t tmem_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
 
   long long at = sh.size * cta;
   const long long stop = min(sh.total, at + sh.size);
   int4 desc = make_int4(0, 0, 0, 0);
   int b = sh.b;
   long long into = sh.into;
-  uint32_t steps = 0, items = 0;  // so far: the barriers' phases
+  // the barriers' phases: steps of the keys, of each tile, and items of each tile
+  uint32_t steps = 0, tile_steps[2] = {0, 0}, tile_items[2] = {0, 0};
   const int l = tid % LPR;
-  const LaneTurn turn = lane_turn(a.r, l);
   T* stage_row = reinterpret_cast<T*>(sm + S::kRowStage) + (tid / LPR) * D;
   const int plog = 31 - __clz(a.c.page);
 
@@ -320,23 +324,32 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
       continue;
     }
     const Part part = find_part<kRows, KT, kStart>(a, s, per_head, into, stop - at);
-    const int h = part.h, qt = part.qt, keys = part.keys, t0 = part.t0, take = part.t1 - part.t0;
-    const bool first = t0 == 0, last = part.t1 == part.tiles;
+    const int h = part.h, qt = part.qt, keys = part.keys, take = part.t1 - part.t0;
+    const bool first = part.t0 == 0, last = part.t1 == part.tiles;
     const size_t slot = ((size_t)2 * cta + (first ? 1 : 0)) * kRows;
     const long long item_end = at - into + part.end;
     at += part.units;
     into += part.units;
     if (take == 0) {  // no key tile: nothing to do, but a piece that the join counts on says so
-      if (t0 > 0 && tid < kRows) *reinterpret_cast<float2*>(a.stat + 2 * (slot + tid)) = make_float2(-INFINITY, 0.0f);
+      if (part.t0 > 0 && tid < kRows)
+        *reinterpret_cast<float2*>(a.stat + 2 * (slot + tid)) = make_float2(-INFINITY, 0.0f);
       continue;
     }
     const int rows = min(kRows, s.rows - qt * kRows);
-    const int tok0 = t0 * KT;
+    const int tok0 = part.t0 * KT;
+    // steps of each tile: the second may have no rows, the first may see fewer keys
+    int tile_take[2] = {take, rows > kTileRows ? take : 0};
+    if (a.causal && rows > kTileRows) {
+      const int seen = max(1, s.len - s.n + row_token(a, qt * kRows + kTileRows - 1) + 1);
+      tile_take[0] = min(take, max(0, (seen + KT - 1) / KT - part.t0));
+    }
 
-    // the item's query rows: turned, scaled by a power of two, fp16, as an operand
     constexpr int PASS = 256 / LPR, BATCH = 4;
     if (warp < 8) {
-      for (int p = 0; p < kRows; p += BATCH * PASS) {
+      // the item's query rows: turned, scaled by a power of two, fp16, as operands
+      const LaneTurn turn = lane_turn(a.r, l);
+      if (tid >= rows) row_fac[tid] = 0.0f, row_lim[tid] = 0x7FFFFFFF;  // not there: not masked, not used
+      for (int p = 0; p < rows; p += BATCH * PASS) {
         uint4 w[BATCH];
         int token[BATCH];
 #pragma unroll
@@ -370,7 +383,9 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] *= f;
           const uint4 hi = pack8<__half>(x);
-          const uint32_t to = (uint32_t)((l >> 3) * (kRows * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4));
+          const int tr = r & (kTileRows - 1);
+          const uint32_t to = (uint32_t)((r / kTileRows) * S::kTileQ + (l >> 3) * (kTileRows * 128) + tr * 128 +
+                                         (((l & 7) ^ (tr & 7)) << 4));
           sts128(base + S::kQuery + to, hi.x, hi.y, hi.z, hi.w);
           if constexpr (TWO) {
             float y[8];
@@ -380,25 +395,27 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
             const uint4 lo = pack8<__half>(y);
             sts128(base + S::kLow + to, lo.x, lo.y, lo.z, lo.w);
           }
-          if (l == 0) {
+          if (l == 0 && r < rows) {
             row_fac[r] = pow2(e) * a.scale;
-            // a row that is not there is not masked, and not used
-            row_lim[r] = r >= rows ? 0x7FFFFFFF : a.causal ? s.len - s.n + token[k] + 1 : s.len;
+            row_lim[r] = a.causal ? s.len - s.n + token[k] + 1 : s.len;
           }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    __syncthreads();
 
-    if (warp >= 4 && warp < 8) {
+    if (warp >= 8 && warp < 12) {
       // ---- expanding the codes ----
-      constexpr int NH = KT / 64;           // pieces of 64 keys
-      const int ct = tid - 128;
-      const int kn = ct & 63, kh = ct >> 6;  // a token's row, which half of it
-      const int vc = ct & 7, vg = ct >> 3;   // eight tokens, D / 16 coordinates
-      constexpr int KW = D / 32;             // 16-byte vectors of codes of half a row
-      constexpr int VW = D / 64;             // words of D / 16 codes
+      // Keys: eight lanes beside one another have two rows' 16-byte pieces of one
+      // 128-byte block, which lie in different banks.  Values: a lane takes eight
+      // tokens and VB bytes of each; eight lanes beside one another have eight token
+      // groups, whose chunks lie in different banks.
+      const int ct = tid - 256;
+      constexpr int KP = (KT / 32) * (D / 64);         // 16-byte pieces of keys of a lane
+      constexpr int VB = KT * D / 1024, VW = VB / 4;   // bytes and words of a token's values
+      const int kr = ct >> 2, kc = ct & 3;
+      const int vt = 8 * (warp & 1) + (lane & 7);
+      const int vd = (((warp - 8) >> 1) * 4 + (lane >> 3)) * VB;
       const int* table = a.table + (size_t)b * a.width;
       auto row_at = [&](int tok) -> size_t {  // row of codes of a token (some row where there is none)
         int page = 0;
@@ -408,24 +425,30 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
         }
         return (((size_t)page * a.c.heads + h) << plog) + (tok & (a.c.page - 1));
       };
-      uint32_t code[NH][D / 8];  // of the keys' piece or the values', whichever comes next
-      auto load_k = [&](int t, int i) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.c.k + row_at(tok0 + t * KT + 64 * i + kn) * D + kh * (D / 2));
+      uint32_t code[4 * KP];  // of the keys or the values, whichever comes next
+      static_assert(8 * VW == 4 * KP, "as many codes either way");
+      auto load_k = [&](int t) {
 #pragma unroll
-        for (int j = 0; j < KW; ++j) {
-          const uint4 w = p[j];
-          code[i][4 * j] = w.x, code[i][4 * j + 1] = w.y, code[i][4 * j + 2] = w.z, code[i][4 * j + 3] = w.w;
+        for (int i = 0; i < KT / 32; ++i) {
+          const int8_t* p = a.c.k + row_at(tok0 + t * KT + 32 * i + kr) * D + 16 * kc;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + 64 * j);
+            uint32_t* to = code + 4 * (i * (D / 64) + j);
+            to[0] = w.x, to[1] = w.y, to[2] = w.z, to[3] = w.w;
+          }
         }
       };
-      auto load_v = [&](int t, int i) {
-        const int8_t* p = a.c.v + row_at(tok0 + t * KT + 64 * i + 8 * vc) * D + vg * (D / 16);
+      auto load_v = [&](int t) {
+        const int8_t* p = a.c.v + row_at(tok0 + t * KT + 8 * vt) * D + vd;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if constexpr (VW == 2) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p + j * D);
-            code[i][2 * j] = w.x, code[i][2 * j + 1] = w.y;
+          if constexpr (VW == 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + j * D);
+            code[4 * j] = w.x, code[4 * j + 1] = w.y, code[4 * j + 2] = w.z, code[4 * j + 3] = w.w;
           } else {
-            code[i][j] = *reinterpret_cast<const uint32_t*>(p + j * D);
+            const uint2 w = *reinterpret_cast<const uint2*>(p + j * D);
+            code[2 * j] = w.x, code[2 * j + 1] = w.y;
           }
         }
       };
@@ -443,120 +466,146 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
           }
         }
       };
-#pragma unroll
-      for (int i = 0; i < NH; ++i) load_k(0, i);
+      load_k(0);
       if (ct < KT / 16) load_scales(0);
+      __syncthreads();
       for (int t = 0; t < take; ++t) {
-        const uint32_t it = steps + t, ph = it & 1u;
-        wait_bounded(bar(K_EMPTY), ph ^ 1u, abort_flag, a.status);
+        const uint32_t it = steps + t;
+        wait_bounded(bar(K_EMPTY), (it & 1u) ^ 1u, abort_flag, a.status);
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
+        for (int i = 0; i < KT / 32; ++i) {
+          const int n = 32 * i + kr;
 #pragma unroll
-          for (int j = 0; j < KW; ++j) {
+          for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {  // eight codes: one 16-byte chunk of the row's 128-byte blocks
-              const uint32_t w0 = code[i][4 * j + 2 * u] ^ 0x80808080u, w1 = code[i][4 * j + 2 * u + 1] ^ 0x80808080u;
-              const int chunk = kh * (D / 16) + 2 * j + u;
-              sts128(base + S::kKeys + (chunk >> 3) * (KT * 128) + (64 * i + kn) * 128 + (((chunk & 7) ^ (kn & 7)) << 4),
-                     bytes2(w0, 0x4140), bytes2(w0, 0x4342), bytes2(w1, 0x4140), bytes2(w1, 0x4342));
+            for (int u = 0; u < 2; ++u) {  // eight codes: one 16-byte chunk
+              const uint32_t* w = code + 4 * (i * (D / 64) + j) + 2 * u;
+              const uint32_t w0 = w[0] ^ 0x80808080u, w1 = w[1] ^ 0x80808080u;
+              sts128(base + S::kKeys + j * (KT * 128) + n * 128 + (((2 * kc + u) ^ (n & 7)) << 4), bytes2(w0, 0x4140),
+                     bytes2(w0, 0x4342), bytes2(w1, 0x4140), bytes2(w1, 0x4342));
             }
-          }
-          load_v(t, i);
         }
+        load_v(t);
         if (ct < KT / 16) {
           const int ev = min(max(scale_exp(sc.y), -126), 126);
-          scales[ph * (KT / 16) + ct] = make_float4(sc.x, (float)ev, pow2(-ev), 0.0f);
+          scales[(it & 1u) * (KT / 16) + ct] = make_float4(sc.x, (float)ev, pow2(-ev), 0.0f);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(K_FULL));
         if (t + 1 < take && ct < KT / 16) load_scales(t + 1);
 
-        wait_bounded(bar(V_EMPTY), ph ^ 1u, abort_flag, a.status);
+        const uint32_t st = it % VST;
+        wait_bounded(bar(V_EMPTY + st), ((it / VST) & 1u) ^ 1u, abort_flag, a.status);
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
+        for (int w = 0; w < VW; ++w) {
+          uint32_t o[4][4];  // [coordinate][pair of tokens]
 #pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            uint32_t o[4][4];  // [coordinate][pair of tokens]
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t x0 = code[i][VW * (2 * q) + w] ^ 0x80808080u, x1 = code[i][VW * (2 * q + 1) + w] ^ 0x80808080u;
-              const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
-              o[0][q] = bytes2(lo, 0x4140), o[1][q] = bytes2(lo, 0x4342);
-              o[2][q] = bytes2(hi, 0x4140), o[3][q] = bytes2(hi, 0x4342);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int d = vg * (D / 16) + 4 * w + k;
-              sts128(base + S::kValues + i * (D * 128) + d * 128 + ((vc ^ (d & 7)) << 4), o[k][0], o[k][1], o[k][2], o[k][3]);
-            }
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t x0 = code[VW * (2 * q) + w] ^ 0x80808080u, x1 = code[VW * (2 * q + 1) + w] ^ 0x80808080u;
+            const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
+            o[0][q] = bytes2(lo, 0x4140), o[1][q] = bytes2(lo, 0x4342);
+            o[2][q] = bytes2(hi, 0x4140), o[3][q] = bytes2(hi, 0x4342);
           }
-          if (t + 1 < take) load_k(t + 1, i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int d = vd + 4 * w + k;
+            sts128(base + S::kValues + st * S::kOperand + (vt >> 3) * (D * 128) + d * 128 + (((vt & 7) ^ (d & 7)) << 4),
+                   o[k][0], o[k][1], o[k][2], o[k][3]);
+          }
         }
+        if (t + 1 < take) load_k(t + 1);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(V_FULL));
+        if (lane == 0) mbar_arrive(bar(V_FULL + st));
       }
-    } else if (warp == 8) {
-      // ---- products ----
-      const uint64_t qd = desc_sw128(base + S::kQuery), ld = desc_sw128(base + S::kLow);
-      const uint64_t kd = desc_sw128(base + S::kKeys), vd = desc_sw128(base + S::kValues);
-      for (int t = 0; t < take; ++t) {
-        const uint32_t ph = (steps + t) & 1u;
-        wait_bounded(bar(K_FULL), ph, abort_flag, a.status);
+    } else if (warp == 12) {
+      // ---- products: a tile's sum, then its next scores, while the other tile's weights are made ----
+      __syncthreads();
+      const uint64_t kd = desc_sw128(base + S::kKeys), vd0 = desc_sw128(base + S::kValues);
+      auto scores = [&](int w, int t) {
+        if (t == 0 || w == 0 || tile_take[0] <= t) wait_bounded(bar(K_FULL), (steps + t) & 1u, abort_flag, a.status);
         __syncwarp();
         tc_fence_after();
         if (elect_one()) {
+          const uint64_t qd = desc_sw128(base + S::kQuery + w * S::kTileQ);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss<KT>(tmem + kColS, qd + (uint64_t)((k >> 2) * (kRows * 8) + (k & 3) * 2),
+            mma_ss<KT>(tmem + kColS + 128 * w, qd + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
                        kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), k > 0);
           if constexpr (TWO) {
+            const uint64_t ld = desc_sw128(base + S::kLow + w * S::kTileQ);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              mma_ss<KT>(tmem + kColS, ld + (uint64_t)((k >> 2) * (kRows * 8) + (k & 3) * 2),
+              mma_ss<KT>(tmem + kColS + 128 * w, ld + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
                          kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), 1u);
           }
-          commit(bar(K_EMPTY));
-          commit(bar(S_FULL));
+          commit(bar(S_FULL + w));
         }
         __syncwarp();
-        wait_bounded(bar(V_FULL), ph, abort_flag, a.status);
+      };
+      auto keys_done = [&]() {
+        if (elect_one()) commit(bar(K_EMPTY));
+        __syncwarp();
+      };
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          wait_bounded(bar(P_FULL + hf), ph, abort_flag, a.status);
-          __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
+      for (int w = 0; w < 2; ++w)
+        if (tile_take[w] > 0) scores(w, 0);
+      keys_done();
+      for (int t = 0; t < take; ++t) {
+        const uint32_t it = steps + t, st = it % VST;
+        wait_bounded(bar(V_FULL + st), (it / VST) & 1u, abort_flag, a.status);
 #pragma unroll
-            for (int k = hf * (HK / 16); k < (hf + 1) * (HK / 16); ++k)
-              mma_ts<D>(tmem + kColO, tmem + kColS + 8 * k, vd + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), t > 0 || k > 0);
-            if (hf == 0) {
-              commit(bar(HALF));
-            } else {
-              commit(bar(V_EMPTY));
-              if (t + 1 == take) commit(bar(O_FULL));
+        for (int w = 0; w < 2; ++w) {
+          if (t < tile_take[w]) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              wait_bounded(bar(P_FULL + 2 * w + hf), (tile_steps[w] + t) & 1u, abort_flag, a.status);
+              __syncwarp();
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t vd = vd0 + (uint64_t)(st * (S::kOperand / 16));
+#pragma unroll
+                for (int k = hf * (HK / 16); k < (hf + 1) * (HK / 16); ++k)
+                  mma_ts<D>(tmem + kColO + 128 * w, tmem + kColS + 128 * w + 8 * k,
+                            vd + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), t > 0 || k > 0);
+                if (hf == 0)
+                  commit(bar(HALF + w));
+                else if (t + 1 == tile_take[w])
+                  commit(bar(O_FULL + w));
+              }
+              __syncwarp();
             }
           }
-          __syncwarp();
+          if (w == 1) {
+            if (elect_one()) commit(bar(V_EMPTY + st));
+            __syncwarp();
+          }
+          if (t + 1 < tile_take[w]) scores(w, t + 1);
         }
+        if (t + 1 < take) keys_done();
       }
-    } else if (warp < 4) {
+    } else {
       // ---- weights ----
+      __syncthreads();
+      const int w = warp >> 2;
+      const uint32_t tmem_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * w;  // this warp's lanes
       const float fac = row_fac[tid];
       const int lim = row_lim[tid];
+      const int my_take = w ? tile_take[1] : tile_take[0];
+      const uint32_t my_steps = w ? tile_steps[1] : tile_steps[0], my_items = w ? tile_items[1] : tile_items[0];
       float top = 0.0f, sum = 0.0f;
       bool none = true;  // no key seen so far: the maximum says nothing
-      for (int t = 0; t < take; ++t) {
-        const uint32_t it = steps + t, ph = it & 1u;
-        wait_bounded(bar(S_FULL), ph, abort_flag, a.status);
+      for (int t = 0; t < my_take; ++t) {
+        const uint32_t ph = (my_steps + t) & 1u;
+        wait_bounded(bar(S_FULL + w), ph, abort_flag, a.status);
         __syncwarp();
         tc_fence_after();
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const float4* sc = scales + ph * (KT / 16) + hf * (HK / 16);
+          const float4* sc = scales + ((steps + t) & 1u) * (KT / 16) + hf * (HK / 16);
           const uint32_t from = tmem_row + kColS + HK * hf;
           const int left = lim - (tok0 + t * KT + HK * hf);  // keys of the half that the row may see
           const bool whole = __all_sync(0xFFFFFFFFu, left >= HK);
@@ -579,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
             if (raise) none = false;
             sum *= f;
             if (hf == 1) {  // the first half's products must have been added
-              wait_bounded(bar(HALF), ph, abort_flag, a.status);
+              wait_bounded(bar(HALF + w), ph, abort_flag, a.status);
               __syncwarp();
               tc_fence_after();
             }
@@ -595,36 +644,46 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
               }
             }
           }
-          if constexpr (HK == 64)
-            tmem_st32(tmem_row + kColS + 32 * hf, p);
-          else
-            tmem_st16(tmem_row + kColS + 16 * hf, p);
+          tmem_st32(tmem_row + kColS + 32 * hf, p);
           wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(P_FULL + hf));
+          if (lane == 0) mbar_arrive(bar(P_FULL + 2 * w + hf));
         }
       }
-      wait_bounded(bar(O_FULL), items & 1u, abort_flag, a.status);
-      __syncwarp();
-      tc_fence_after();
-      // the rows' sums into shared memory (the operands' place), 16-byte chunks turned by the row
+      if (my_take > 0) {
+        wait_bounded(bar(O_FULL + w), my_items & 1u, abort_flag, a.status);
+        __syncwarp();
+        tc_fence_after();
+      }
+      row_stat[tid] = make_float2(none && sum == sum ? -INFINITY : top, sum);  // (a NaN query's piece counts)
+    }
+    // The rows' sums go through shared memory, in the operands' place: both tiles are done.
+    __syncthreads();
+    if (warp < 8) {
+      const int w = warp >> 2;
+      const uint32_t tmem_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * w;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
-        tmem_ld32(tmem_row + kColO + c, o);
-        wait_ld();
+        if ((w ? tile_take[1] : tile_take[0]) > 0) {
+          tmem_ld32(tmem_row + kColO + c, o);
+          wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           sts128(base + tid * (D * 4) + (((c / 4 + j) ^ (tid & 7)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
       }
-      row_stat[tid] = make_float2(none && sum == sum ? -INFINITY : top, sum);  // (a NaN query's piece counts)
       tc_fence_before();
     }
     __syncthreads();
     if (warp < 8) {
+      const LaneTurn turn = lane_turn(a.r, l);
 #pragma unroll 2
-      for (int p = 0; p < kRows; p += PASS) {
+      for (int p = 0; p < rows; p += PASS) {
         const int r = p + tid / LPR;
         const float4 lo = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l) ^ (r & 7)) << 4));
         const float4 hi = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l + 1) ^ (r & 7)) << 4));
@@ -655,15 +714,20 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_kernel(const __grid_constan
       }
     }
     if (first && !last) desc = make_int4((int)((item_end - 1) / sh.size) - cta + 1, b, h, qt);
+    tc_fence_after();
     __syncthreads();
     steps += take;
-    ++items;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      tile_steps[w] += tile_take[w];
+      tile_items[w] += tile_take[w] > 0;
+    }
   }
   if (tid == 0) a.desc[cta] = desc;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8)
+  if (warp == 12)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
 }
 
@@ -672,9 +736,6 @@ int launch(const Args& a, cudaStream_t s) {
   using S = Smem<D, TWO>;
   auto kern = chunk_kernel<T, D, TWO>;
   int per_sm = 0, nsm = 0;
-  // (raises the kernel's shared-memory limit; the query itself says one CTA an SM
-  // for a kernel that allocates TMEM, where two share its registers, shared memory
-  // and TMEM by construction; none waits for another)
   if (int rc = occupancy(reinterpret_cast<const void*>(kern), S::kAlloc, kThreads, 0, &per_sm)) return rc;
   if (int rc = sm_count(&nsm)) return rc;
   if (per_sm < 1) return fail(OQ_ERR_UNSUPPORTED, "attention kernel does not fit");
@@ -682,11 +743,11 @@ int launch(const Args& a, cudaStream_t s) {
   const long long rows = (long long)a.T * a.group;
   const long long items = std::min<long long>((rows + kRows - 1) / kRows + a.B, rows) * a.c.heads;
   const long long units = items * (kStart + 1 + (long long)a.width * a.c.page / S::KT);
-  const int ctas = (int)std::min<long long>(units, std::min(2 * nsm, kChunkCtas));
+  const int ctas = (int)std::min<long long>(units, std::min(nsm, kChunkCtas));
   kern<<<ctas, kThreads, S::kAlloc, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-  join_kernel<T, D, kRows><<<dim3((unsigned)ctas, 16), 128, 0, s>>>(a, 0);
+  join_kernel<T, D, kRows><<<dim3((unsigned)ctas, 32), 128, 0, s>>>(a, 0);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention join launch: %s", cudaGetErrorString(e));
   return OQ_OK;

@@ -459,7 +459,7 @@ int launch_step(const Args& a, int ctas_most, cudaStream_t s) {
   kern<<<ctas, kThreads, smem, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-  join_kernel<T, D, 8 * NQ><<<dim3((unsigned)ctas, 8 * NQ), 128, 0, s>>>(a, 0);
+  join_kernel<T, D, 8 * NQ, 4><<<dim3((unsigned)ctas, 8 * NQ), 128, 0, s>>>(a, 0);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention join launch: %s", cudaGetErrorString(e));
   return OQ_OK;

@@ -196,13 +196,16 @@ __device__ __forceinline__ Part find_part(const Args& a, const Seq& s, long long
   return p;
 }
 
-// Puts the pieces of cut items together and writes their rows: block (i, j) the
-// rows j, j + gridDim.y, ... of the item that CTA i began.
-template <typename T, int D, int RT>
+// Puts the pieces of cut items together and writes their rows.  Block (i, j): rows
+// of the item that CTA i began, 4 / WPR of them at a time, each by WPR warps that
+// take turns over the pieces (WPR = 4 where an item may have many pieces, 1 where
+// it has many rows).
+template <typename T, int D, int RT, int WPR>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a, int pdl) {
-  __shared__ float part[4][D];
-  __shared__ float part_sum[4], part_max[4];
-  __shared__ __align__(16) T row_out[D];
+  constexpr int ROWS = 4 / WPR;
+  __shared__ __align__(16) float part[4][D];
+  __shared__ float part_sum[4];
+  __shared__ __align__(16) T row_out[4][D];
   if (pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 d = a.desc[blockIdx.x];
   if (d.x <= 0) return;
@@ -210,25 +213,24 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(RT, s.rows - d.w * RT);
   constexpr int V = D / 32;  // values of a lane
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+  for (int r0 = blockIdx.y * ROWS; r0 < rows; r0 += gridDim.y * ROWS) {
+    const int r = min(r0 + warp / WPR, rows - 1);
     auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * RT + r; };
     float top = -INFINITY;
-    for (int i = threadIdx.x; i < d.x; i += 128) top = fmaxf(top, a.stat[2 * slot(i)]);
+    for (int i = lane; i < d.x; i += 32) top = fmaxf(top, a.stat[2 * slot(i)]);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-    if (lane == 0) part_max[warp] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(part_max[0], part_max[1]), fmaxf(part_max[2], part_max[3]));
     if (top == -INFINITY) top = 0.0f;
     float o[V], sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] = 0.0f;
 #pragma unroll 4
-    for (int i = warp; i < d.x; i += 4) {
+    for (int i = warp % WPR; i < d.x; i += WPR) {
       const size_t at = slot(i);
-      const float f = exp2f(a.stat[2 * at] - top);
+      const float2 st = *reinterpret_cast<const float2*>(a.stat + 2 * at);
+      const float f = exp2f(st.x - top);
       if (f == 0.0f) continue;  // nothing there: its values may not even be written
-      sum = fmaf(f, a.stat[2 * at + 1], sum);
+      sum = fmaf(f, st.y, sum);
       const float* p = a.piece + at * D + V * lane;
       if constexpr (V == 4) {
         const float4 v = *reinterpret_cast<const float4*>(p);
@@ -241,29 +243,42 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
 #pragma unroll
     for (int k = 0; k < V; ++k) part[warp][V * lane + k] = o[k];
     if (lane == 0) part_sum[warp] = sum;
-    __syncthreads();
-    if (warp == 0) {
-      sum = part_sum[0] + part_sum[1] + part_sum[2] + part_sum[3];
-      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // no key: 0; NaN stays
+    if constexpr (WPR == 1)
+      __syncwarp();
+    else
+      __syncthreads();
+    if (warp % WPR == 0) {
       const int l = lane % (D / 8);
       float x[8];
+      sum = part_sum[warp];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        x[k] = ((part[0][8 * l + k] + part[1][8 * l + k]) + (part[2][8 * l + k] + part[3][8 * l + k])) * inv;
+      for (int k = 0; k < 8; ++k) x[k] = part[warp][8 * l + k];
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) {
+        sum += part_sum[warp + w];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] += part[warp + w][8 * l + k];
+      }
+      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // no key: 0; NaN stays
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] *= inv;
       uint4 w;
       if (a.r.perm) {
-        unrotate_row<T>(x, lane_turn(a.r, l), l, a.r, row_out);  // lanes of one l write the same values
+        unrotate_row<T>(x, lane_turn(a.r, l), l, a.r, row_out[warp]);  // lanes of one l write the same values
         __syncwarp();
-        w = *reinterpret_cast<const uint4*>(row_out + 8 * l);
+        w = *reinterpret_cast<const uint4*>(row_out[warp] + 8 * l);
       } else {
         w = pack8<T>(x);
       }
       const int g = d.w * RT + r, i = row_token(a, g);
-      if (lane < D / 8)
+      if (lane < D / 8 && r0 + warp / WPR < rows)
         *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
                                   ((long long)d.z * a.group + (g - i * a.group)) * a.oh + 8 * l) = w;
     }
-    __syncthreads();
+    if constexpr (WPR == 1)
+      __syncwarp();
+    else
+      __syncthreads();
   }
 }
 

@@ -45,6 +45,7 @@ using namespace cattn;
 constexpr int kThreads = 416, kRows = 256, kTileRows = 128;
 constexpr int kTmem = 512, kColS = 0, kColO = 256;  // a tile's columns begin 128 further on
 constexpr int kStart = 4;  // units of an item's beginning and end
+constexpr int kBatch = 4;  // rows that a thread turns at a time, for their latencies' sake
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -208,38 +209,44 @@ __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsig
 template <int KEYS, bool MASKED>
 __device__ __forceinline__ float weigh(uint32_t scores, const float4* sc, float fac, float top, int left,
                                        uint32_t (&p)[KEYS / 2], float& mx) {
-  mx = -INFINITY;
-  float sum = 0.0f;
+  uint32_t v[KEYS];
 #pragma unroll
-  for (int q = 0; q < KEYS / 32; ++q) {
-    uint32_t v[32];
-    tmem_ld32(scores + 32 * q, v);
-    wait_ld();
+  for (int q = 0; q < KEYS / 32; ++q) tmem_ld32(scores + 32 * q, v + 32 * q);
+  float4 s[KEYS / 16];
 #pragma unroll
-    for (int gg = 0; gg < 2; ++gg) {
-      const int g = 2 * q + gg;
-      const float4 s = sc[g];
-      const float c = s.x * fac, d = s.x != 0.0f ? s.y - top : -INFINITY;  // an empty page's scores go
-      const unsigned long long c2 = f2_pack(c, c), d2 = f2_pack(d, d);
-      unsigned long long add = f2_pack(0.0f, 0.0f);
+  for (int g = 0; g < KEYS / 16; ++g) s[g] = sc[g];
+  wait_ld();
+  float most[KEYS / 16], sum = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float x0, x1;
-        f2_split(f2_fma(u2_pack(v[16 * gg + 2 * j], v[16 * gg + 2 * j + 1]), c2, d2), x0, x1);
-        if constexpr (MASKED) {
-          if (16 * g + 2 * j >= left) x0 = -INFINITY;
-          if (16 * g + 2 * j + 1 >= left) x1 = -INFINITY;
-        }
-        mx = fmaxf(mx, fmaxf(x0, x1));
-        const float e0 = ex2(x0), e1 = ex2(x1);
-        add = f2_add(add, f2_pack(e0, e1));
-        p[8 * g + j] = pack2<__half>(e0, e1);
-      }
-      float s0, s1;
-      f2_split(add, s0, s1);
-      sum = fmaf(s0 + s1, s.z, sum);
+  for (int g = 0; g < KEYS / 16; ++g) {
+    const float c = s[g].x * fac, d = s[g].x != 0.0f ? s[g].y - top : -INFINITY;  // an empty page's scores go
+    const unsigned long long c2 = f2_pack(c, c), d2 = f2_pack(d, d);
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f2_split(f2_fma(u2_pack(v[16 * g + 2 * j], v[16 * g + 2 * j + 1]), c2, d2), x[2 * j], x[2 * j + 1]);
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (16 * g + j >= left) x[j] = -INFINITY;
     }
+    float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[2], x[3]);
+#pragma unroll
+    for (int j = 4; j < 16; j += 4) m0 = fmaxf(m0, fmaxf(x[j], x[j + 1])), m1 = fmaxf(m1, fmaxf(x[j + 2], x[j + 3]));
+    most[g] = fmaxf(m0, m1);
+    unsigned long long add[2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float e0 = ex2(x[2 * j]), e1 = ex2(x[2 * j + 1]);
+      add[j & 1] = j < 2 ? f2_pack(e0, e1) : f2_add(add[j & 1], f2_pack(e0, e1));
+      p[8 * g + j] = pack2<__half>(e0, e1);
+    }
+    float s0, s1;
+    f2_split(f2_add(add[0], add[1]), s0, s1);
+    sum = fmaf(s0 + s1, s[g].z, sum);
   }
+  mx = most[0];
+#pragma unroll
+  for (int g = 1; g < KEYS / 16; ++g) mx = fmaxf(mx, most[g]);
   return sum;
 }
 
@@ -251,14 +258,17 @@ struct Smem {
   static constexpr int kTileQ = kTileRows * D * 2;           // of a tile's queries
   static constexpr int kKeys = 0, kValues = kOperand, kQuery = (1 + VST) * kOperand;
   static constexpr int kLow = kQuery + 2 * kTileQ;           // the queries' second term
-  static constexpr int kRowStage = kLow + (TWO ? 2 * kTileQ : 0);           // 16-bit rows being turned
-  static constexpr int kScales = kRowStage + 256 / (D / 8) * D * 2;         // [2][KT / 16] (key scale, ev, 2^-ev)
+  static constexpr int kScales = kLow + (TWO ? 2 * kTileQ : 0);             // [2][KT / 16] (key scale, ev, 2^-ev)
   static constexpr int kFac = kScales + 2 * (KT / 16) * 16;                 // [rows] factor, limit
   static constexpr int kStat = kFac + kRows * 8;                            // [rows] maximum, sum
   static constexpr int kBars = kStat + kRows * 8;
   static constexpr int kTotal = kBars + 192;
   static constexpr int kAlloc = kTotal + 1024;  // room to align the base
-  static_assert(kRows * D * 4 <= kRowStage, "the rows' sums stand in the operands' place at the end");
+  // Rows being turned, 16 bits a value, eight times 256 threads: in the values'
+  // place before the steps, behind the rows' sums (which take the operands' place)
+  // after them.
+  static constexpr int kTurnIn = kValues, kTurnOut = kRows * D * 4, kTurn = kBatch * 256 * 16;
+  static_assert(kTurn <= kOperand && kTurnOut + kTurn <= kScales, "place for the rows being turned");
   static_assert(kAlloc <= 226 * 1024, "shared memory of a CTA");
 };
 
@@ -312,7 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   // the barriers' phases: steps of the keys, of each tile, and items of each tile
   uint32_t steps = 0, tile_steps[2] = {0, 0}, tile_items[2] = {0, 0};
   const int l = tid % LPR;
-  T* stage_row = reinterpret_cast<T*>(sm + S::kRowStage) + (tid / LPR) * D;
   const int plog = 31 - __clz(a.c.page);
 
   while (at < stop && b < a.B) {
@@ -344,14 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       tile_take[0] = min(take, max(0, (seen + KT - 1) / KT - part.t0));
     }
 
-    constexpr int PASS = 256 / LPR, BATCH = 4;
+    constexpr int PASS = 256 / LPR, BATCH = kBatch;
     if (warp < 8) {
       // the item's query rows: turned, scaled by a power of two, fp16, as operands
       const LaneTurn turn = lane_turn(a.r, l);
       if (tid >= rows) row_fac[tid] = 0.0f, row_lim[tid] = 0x7FFFFFFF;  // not there: not masked, not used
+      T* turn_row = reinterpret_cast<T*>(sm + S::kTurnIn) + (tid / LPR) * D;
       for (int p = 0; p < rows; p += BATCH * PASS) {
         uint4 w[BATCH];
         int token[BATCH];
+        float x[BATCH][8];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
           const int r = p + k * PASS + tid / LPR, gr = qt * kRows + r;
@@ -361,28 +372,35 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             w[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + token[k]) * a.qt +
                                                    ((long long)h * a.group + (gr - token[k] * a.group)) * a.qh + 8 * l);
         }
+        if (a.r.perm) {
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) *reinterpret_cast<uint4*>(turn_row + k * PASS * D + 8 * l) = w[k];
+          __syncwarp();
+          rotate_rows<T, BATCH, PASS * D>(turn_row, turn, l, a.r, x);
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) unpack8<T>(w[k], x[k]);
+        }
+        float top[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          top[k] = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top[k] = fmaxf(top[k], fabsf(x[k][j]));
+        }
+#pragma unroll
+        for (int m = LPR / 2; m >= 1; m >>= 1)
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], m));
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
           const int r = p + k * PASS + tid / LPR;
-          float x[8];
-          if (a.r.perm) {
-            *reinterpret_cast<uint4*>(stage_row + 8 * l) = w[k];
-            __syncwarp();
-            rotate_row<T>(stage_row, turn, l, a.r, x);
-            __syncwarp();
-          } else {
-            unpack8<T>(w[k], x);
-          }
-          float top = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-#pragma unroll
-          for (int m = LPR / 2; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-          const int e = min(max(scale_exp(top), -100), 120);
+          const int e = min(max(scale_exp(top[k]), -100), 120);
           const float f = pow2(-e);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] *= f;
-          const uint4 hi = pack8<__half>(x);
+          for (int j = 0; j < 8; ++j) x[k][j] *= f;
+          const uint4 hi = pack8<__half>(x[k]);
           const int tr = r & (kTileRows - 1);
           const uint32_t to = (uint32_t)((r / kTileRows) * S::kTileQ + (l >> 3) * (kTileRows * 128) + tr * 128 +
                                          (((l & 7) ^ (tr & 7)) << 4));
@@ -391,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             float y[8];
             unpack8<__half>(hi, y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = x[j] - y[j];
+            for (int j = 0; j < 8; ++j) y[j] = x[k][j] - y[j];
             const uint4 lo = pack8<__half>(y);
             sts128(base + S::kLow + to, lo.x, lo.y, lo.z, lo.w);
           }
@@ -682,34 +700,54 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     __syncthreads();
     if (warp < 8) {
       const LaneTurn turn = lane_turn(a.r, l);
-#pragma unroll 2
-      for (int p = 0; p < rows; p += PASS) {
-        const int r = p + tid / LPR;
-        const float4 lo = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l) ^ (r & 7)) << 4));
-        const float4 hi = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l + 1) ^ (r & 7)) << 4));
-        float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const float2 stat = row_stat[r];
-        if (first && last) {
-          const float inv = stat.y > 0.0f ? 1.0f / stat.y : stat.y == 0.0f ? 0.0f : stat.y;
+      T* turn_row = reinterpret_cast<T*>(sm + S::kTurnOut) + (tid / LPR) * D;
+      for (int p = 0; p < rows; p += BATCH * PASS) {
+        float x[BATCH][8];
+        float2 stat[BATCH];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] *= inv;
-          uint4 w;
+        for (int k = 0; k < BATCH; ++k) {
+          const int r = p + k * PASS + tid / LPR;
+          const float4 lo = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l) ^ (r & 7)) << 4));
+          const float4 hi = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l + 1) ^ (r & 7)) << 4));
+          x[k][0] = lo.x, x[k][1] = lo.y, x[k][2] = lo.z, x[k][3] = lo.w;
+          x[k][4] = hi.x, x[k][5] = hi.y, x[k][6] = hi.z, x[k][7] = hi.w;
+          stat[k] = row_stat[r];
+        }
+        if (first && last) {
+          uint4 w[BATCH];
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const float y = stat[k].y, inv = y > 0.0f ? 1.0f / y : y == 0.0f ? 0.0f : y;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[k][j] *= inv;
+          }
           if (a.r.perm) {
-            unrotate_row<T>(x, turn, l, a.r, stage_row);
+            unrotate_rows<T, BATCH, PASS * D>(x, turn, l, a.r, turn_row);
             __syncwarp();
-            w = *reinterpret_cast<const uint4*>(stage_row + 8 * l);
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) w[k] = *reinterpret_cast<const uint4*>(turn_row + k * PASS * D + 8 * l);
             __syncwarp();
           } else {
-            w = pack8<T>(x);
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) w[k] = pack8<T>(x[k]);
           }
-          const int gr = qt * kRows + r, i = row_token(a, gr);
-          if (r < rows)
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
-                                      ((long long)h * a.group + (gr - i * a.group)) * a.oh + 8 * l) = w;
-        } else if (r < rows) {
-          float4* o = reinterpret_cast<float4*>(a.piece + (slot + r) * D + 8 * l);
-          o[0] = lo, o[1] = hi;
-          if (l == 0) *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = stat;
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int r = p + k * PASS + tid / LPR, gr = qt * kRows + r, i = row_token(a, gr);
+            if (r < rows)
+              *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
+                                        ((long long)h * a.group + (gr - i * a.group)) * a.oh + 8 * l) = w[k];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int r = p + k * PASS + tid / LPR;
+            if (r >= rows) continue;
+            float4* o = reinterpret_cast<float4*>(a.piece + (slot + r) * D + 8 * l);
+            o[0] = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+            o[1] = make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
+            if (l == 0) *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = stat[k];
+          }
         }
       }
     }
@@ -747,7 +785,7 @@ int launch(const Args& a, cudaStream_t s) {
   kern<<<ctas, kThreads, S::kAlloc, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-  join_kernel<T, D, kRows><<<dim3((unsigned)ctas, 32), 128, 0, s>>>(a, 0);
+  join_kernel<T, D, kRows, 1><<<dim3((unsigned)ctas, kRows / 4), 128, 0, s>>>(a, 0);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention join launch: %s", cudaGetErrorString(e));
   return OQ_OK;

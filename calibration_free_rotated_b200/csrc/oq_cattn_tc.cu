@@ -15,7 +15,11 @@
 // TMEM, all 512 columns: each tile's scores (KT columns), whose first half the
 // weights take over (the left operand of the sum), and each tile's sum (D
 // columns), which stays until the end.  The turned queries (fp16) are
-// shared-memory operands.  (Two CTAs an SM of one tile each, which expand the
+// shared-memory operands.  The turns themselves are products too: the rows as they
+// come times the matrix Pi (entries 0, 1, -1: exact), and at the end the sums, as
+// two terms of the tensor's type (2^-17 and better), times its transpose; the
+// matrix is written into the values' place when it is needed.  (Butterflies on the
+// 256 rows took 33 thousand clocks an item, a tenth of a long one.)  (Two CTAs an SM of one tile each, which expand the
 // codes twice, took 1.9 times as long: issue slots and the level-1 cache.)
 //
 // Scales: as in oq_cattn.cu the running maximum is taken over score + ev, so
@@ -34,6 +38,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "oq_cattn.cuh"
 
@@ -45,7 +50,6 @@ using namespace cattn;
 constexpr int kThreads = 416, kRows = 256, kTileRows = 128;
 constexpr int kTmem = 512, kColS = 0, kColO = 256;  // a tile's columns begin 128 further on
 constexpr int kStart = 4;  // units of an item's beginning and end
-constexpr int kBatch = 4;  // rows that a thread turns at a time, for their latencies' sake
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -114,6 +118,11 @@ template <int N>
 __host__ __device__ constexpr uint32_t idesc() {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
+// The same with the type of a tensor's rows (the turn's products).
+template <typename T, int N>
+__host__ __device__ constexpr uint32_t idesc_of() {
+  return idesc<N>() | (std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u);
+}
 template <int N>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
   asm volatile(
@@ -123,13 +132,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc<N>()), "r"(accumulate)
       : "memory");
 }
-template <int N>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc<N>()), "r"(accumulate)
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -177,6 +185,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* v) {
       : "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ unsigned long long f2_pack(float lo, float hi) {
   unsigned long long r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -250,6 +263,35 @@ __device__ __forceinline__ float weigh(uint32_t scores, const float4* sc, float 
   return sum;
 }
 
+// A block Hadamard matrix's column in the rows' order: coordinate pi(j) has j here,
+// and the sign of j in bit 15.
+__device__ __forceinline__ void invert(const Rotation& r, uint16_t* inv, int tid, int d) {
+  if (r.perm && tid < d) inv[r.perm[tid]] = (uint16_t)(tid | ((r.signs[tid >> 5] >> (tid & 31) & 1u) << 15));
+}
+// Eight entries (16 bits each, `one` is 1 in their type) of Pi without its factor
+// 1 / sqrt h, as a chunk of a K-major operand: row j, columns 8 c + 0..7 of Pi, or
+// (TRANSPOSED) row i, columns 8 c + 0..7 of its transpose.
+template <bool TRANSPOSED>
+__device__ __forceinline__ uint4 turn_chunk(const uint16_t* inv, int row, int c, int h, uint32_t one) {
+  uint32_t o[4];
+  const uint4 w = TRANSPOSED ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(inv + 8 * c);
+  const uint32_t its[4] = {w.x, w.y, w.z, w.w};
+  const uint32_t own = TRANSPOSED ? inv[row] : 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t e[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t code = TRANSPOSED ? own : (its[k] >> (16 * u)) & 0xFFFFu;
+      const uint32_t j = code & 0x7FFFu, j2 = TRANSPOSED ? 8u * c + 2 * k + u : (uint32_t)row;
+      const uint32_t sign = (code ^ ((uint32_t)__popc(j & j2 & (uint32_t)(h - 1)) << 15)) & 0x8000u;
+      e[u] = ((j ^ j2) & ~(uint32_t)(h - 1)) ? 0u : one | sign;
+    }
+    o[k] = e[0] | e[1] << 16;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 template <int D, bool TWO>
 struct Smem {
   static constexpr int KT = 128;                             // keys of a step
@@ -259,17 +301,18 @@ struct Smem {
   static constexpr int kKeys = 0, kValues = kOperand, kQuery = (1 + VST) * kOperand;
   static constexpr int kLow = kQuery + 2 * kTileQ;           // the queries' second term
   static constexpr int kScales = kLow + (TWO ? 2 * kTileQ : 0);             // [2][KT / 16] (key scale, ev, 2^-ev)
-  static constexpr int kFac = kScales + 2 * (KT / 16) * 16;                 // [rows] factor, limit
-  static constexpr int kStat = kFac + kRows * 8;                            // [rows] maximum, sum
+  static constexpr int kInverse = kScales + 2 * (KT / 16) * 16;             // [D] 16 bits: see invert
+  static constexpr int kStat = kInverse + 2 * D;                            // [rows] maximum, sum
   static constexpr int kBars = kStat + kRows * 8;
   static constexpr int kTotal = kBars + 192;
   static constexpr int kAlloc = kTotal + 1024;  // room to align the base
-  // Rows being turned, 16 bits a value, eight times 256 threads: in the values'
-  // place before the steps, behind the rows' sums (which take the operands' place)
-  // after them.
-  static constexpr int kTurnIn = kValues, kTurnOut = kRows * D * 4, kTurn = kBatch * 256 * 16;
-  static_assert(kTurn <= kOperand && kTurnOut + kTurn <= kScales, "place for the rows being turned");
-  static_assert(kAlloc <= 226 * 1024, "shared memory of a CTA");
+  // Outside the steps: the matrix in the values' first stage; the sums' second terms
+  // in the queries' second terms' place, or the keys' and the values' second stage.
+  static constexpr int kMatrix = kValues;
+  static constexpr int kSumLow0 = TWO ? kLow : kKeys, kSumLow1 = TWO ? kLow + kTileQ : kValues + kOperand;
+  static_assert(D * D * 2 <= kOperand && kTileQ <= kOperand, "what stands in the operands' place");
+  static_assert(kRows * D * 4 <= kScales, "the rows' sums stand in the operands' place at the end");
+  static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
 };
 
 template <typename T, int D, bool TWO>
@@ -280,16 +323,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   unsigned char* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float* row_fac = reinterpret_cast<float*>(sm + S::kFac);
-  int* row_lim = reinterpret_cast<int*>(sm + S::kFac) + kRows;
+  uint16_t* inv = reinterpret_cast<uint16_t*>(sm + S::kInverse);
   float2* row_stat = reinterpret_cast<float2*>(sm + S::kStat);
   float4* scales = reinterpret_cast<float4*>(sm + S::kScales);
   const uint32_t bars = base + S::kBars;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + S::kBars + 176);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 180);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + S::kBars + 160);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 164);
   auto bar = [&](int i) { return bars + 8u * i; };
   // of the two tiles (S_FULL + w) and of a tile's halves (P_FULL + 2 w + half)
-  constexpr int K_FULL = 0, K_EMPTY = 1, V_FULL = 2, V_EMPTY = 4, S_FULL = 6, P_FULL = 8, HALF = 12, O_FULL = 14;
+  constexpr int K_FULL = 0, K_EMPTY = 1, V_FULL = 2, V_EMPTY = 4, S_FULL = 6, P_FULL = 8, HALF = 12, O_FULL = 14, TURN = 16;
 
   if (tid == 0) {
     mbar_init(bar(K_FULL), 4), mbar_init(bar(K_EMPTY), 1);
@@ -297,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       mbar_init(bar(V_FULL + i), 4), mbar_init(bar(V_EMPTY + i), 1);
       mbar_init(bar(S_FULL + i), 1), mbar_init(bar(HALF + i), 1), mbar_init(bar(O_FULL + i), 1);
       mbar_init(bar(P_FULL + 2 * i), 4), mbar_init(bar(P_FULL + 2 * i + 1), 4);
+      mbar_init(bar(TURN + i), 1);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -307,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  invert(a.r, inv, tid, D);
   const int cta = blockIdx.x;
   const Share sh = find_share<kRows, KT, kStart, kThreads>(a, cta, gridDim.x);
   tc_fence_before();
@@ -319,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   int4 desc = make_int4(0, 0, 0, 0);
   int b = sh.b;
   long long into = sh.into;
-  // the barriers' phases: steps of the keys, of each tile, and items of each tile
-  uint32_t steps = 0, tile_steps[2] = {0, 0}, tile_items[2] = {0, 0};
+  // the barriers' phases: steps of the keys, of each tile, items of each tile, turns
+  uint32_t steps = 0, tile_steps[2] = {0, 0}, tile_items[2] = {0, 0}, turns = 0;
   const int l = tid % LPR;
   const int plog = 31 - __clz(a.c.page);
 
@@ -353,73 +397,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       tile_take[0] = min(take, max(0, (seen + KT - 1) / KT - part.t0));
     }
 
-    constexpr int PASS = 256 / LPR, BATCH = kBatch;
+    const int tiles = rows > kTileRows ? 2 : 1;
+    const bool turned = a.r.perm != nullptr;
+    constexpr uint32_t one = std::is_same<T, __nv_bfloat16>::value ? 0x3F80u : 0x3C00u;
+    constexpr int PASS = 256 / LPR, BATCH = 8;
     if (warp < 8) {
-      // the item's query rows: turned, scaled by a power of two, fp16, as operands
-      const LaneTurn turn = lane_turn(a.r, l);
-      if (tid >= rows) row_fac[tid] = 0.0f, row_lim[tid] = 0x7FFFFFFF;  // not there: not masked, not used
-      T* turn_row = reinterpret_cast<T*>(sm + S::kTurnIn) + (tid / LPR) * D;
-      for (int p = 0; p < rows; p += BATCH * PASS) {
+      // the item's query rows as they come, as operands
+      for (int p = 0; p < tiles * kTileRows; p += BATCH * PASS) {
         uint4 w[BATCH];
-        int token[BATCH];
-        float x[BATCH][8];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-          const int r = p + k * PASS + tid / LPR, gr = qt * kRows + r;
-          token[k] = row_token(a, gr);
+          const int r = p + k * PASS + tid / LPR, gr = qt * kRows + r, i = row_token(a, gr);
           w[k] = make_uint4(0u, 0u, 0u, 0u);
           if (r < rows)
-            w[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + token[k]) * a.qt +
-                                                   ((long long)h * a.group + (gr - token[k] * a.group)) * a.qh + 8 * l);
+            w[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + i) * a.qt +
+                                                   ((long long)h * a.group + (gr - i * a.group)) * a.qh + 8 * l);
         }
-        if (a.r.perm) {
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) *reinterpret_cast<uint4*>(turn_row + k * PASS * D + 8 * l) = w[k];
-          __syncwarp();
-          rotate_rows<T, BATCH, PASS * D>(turn_row, turn, l, a.r, x);
-          __syncwarp();
-        } else {
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) unpack8<T>(w[k], x[k]);
-        }
-        float top[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-          top[k] = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) top[k] = fmaxf(top[k], fabsf(x[k][j]));
-        }
-#pragma unroll
-        for (int m = LPR / 2; m >= 1; m >>= 1)
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], m));
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          const int r = p + k * PASS + tid / LPR;
-          const int e = min(max(scale_exp(top[k]), -100), 120);
-          const float f = pow2(-e);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[k][j] *= f;
-          const uint4 hi = pack8<__half>(x[k]);
-          const int tr = r & (kTileRows - 1);
-          const uint32_t to = (uint32_t)((r / kTileRows) * S::kTileQ + (l >> 3) * (kTileRows * 128) + tr * 128 +
-                                         (((l & 7) ^ (tr & 7)) << 4));
-          sts128(base + S::kQuery + to, hi.x, hi.y, hi.z, hi.w);
-          if constexpr (TWO) {
-            float y[8];
-            unpack8<__half>(hi, y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = x[k][j] - y[j];
-            const uint4 lo = pack8<__half>(y);
-            sts128(base + S::kLow + to, lo.x, lo.y, lo.z, lo.w);
-          }
-          if (l == 0 && r < rows) {
-            row_fac[r] = pow2(e) * a.scale;
-            row_lim[r] = a.causal ? s.len - s.n + token[k] + 1 : s.len;
-          }
+          const int r = p + k * PASS + tid / LPR, tr = r & (kTileRows - 1);
+          sts128(base + S::kQuery + (r / kTileRows) * S::kTileQ + (l >> 3) * (kTileRows * 128) + tr * 128 +
+                     (((l & 7) ^ (tr & 7)) << 4),
+                 w[k].x, w[k].y, w[k].z, w[k].w);
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
 
     if (warp >= 8 && warp < 12) {
@@ -486,6 +487,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       };
       load_k(0);
       if (ct < KT / 16) load_scales(0);
+      if (turned)
+        for (int c = tid - 256; c < D * LPR; c += 160) {
+          const uint4 w = turn_chunk<false>(inv, c / LPR, c % LPR, a.r.h, one);
+          sts128(base + S::kMatrix + ((c % LPR) >> 3) * (D * 128) + (c / LPR) * 128 + (((c & 7) ^ (c / LPR & 7)) << 4), w.x, w.y,
+                 w.z, w.w);
+        }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
       for (int t = 0; t < take; ++t) {
         const uint32_t it = steps + t;
@@ -515,6 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (t + 1 < take && ct < KT / 16) load_scales(t + 1);
 
         const uint32_t st = it % VST;
+        if (t == 0 && turned) {  // the matrix stands in the values' place
+          wait_bounded(bar(TURN), turns & 1u, abort_flag, a.status);
+          wait_bounded(bar(TURN + 1), turns & 1u, abort_flag, a.status);
+        }
         wait_bounded(bar(V_EMPTY + st), ((it / VST) & 1u) ^ 1u, abort_flag, a.status);
         __syncwarp();
 #pragma unroll
@@ -541,7 +553,33 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
     } else if (warp == 12) {
       // ---- products: a tile's sum, then its next scores, while the other tile's weights are made ----
+      if (turned)
+        for (int c = tid - 256; c < D * LPR; c += 160) {
+          const uint4 w = turn_chunk<false>(inv, c / LPR, c % LPR, a.r.h, one);
+          sts128(base + S::kMatrix + ((c % LPR) >> 3) * (D * 128) + (c / LPR) * 128 + (((c & 7) ^ (c / LPR & 7)) << 4), w.x, w.y,
+                 w.z, w.w);
+        }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
+      const uint64_t md = desc_sw128(base + S::kMatrix);
+      if (turned) {
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint64_t qd = desc_sw128(base + S::kQuery + w * S::kTileQ);
+            if (w < tiles) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(tmem + kColS + 128 * w, qd + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
+                       md + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), idesc_of<T, D>(), k > 0);
+            }
+            commit(bar(TURN + w));
+          }
+        }
+        __syncwarp();
+      }
+      asm volatile("bar.sync 1, 288;" ::: "memory");  // with the rows' warps: the queries stand
       const uint64_t kd = desc_sw128(base + S::kKeys), vd0 = desc_sw128(base + S::kValues);
       auto scores = [&](int w, int t) {
         if (t == 0 || w == 0 || tile_take[0] <= t) wait_bounded(bar(K_FULL), (steps + t) & 1u, abort_flag, a.status);
@@ -551,14 +589,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const uint64_t qd = desc_sw128(base + S::kQuery + w * S::kTileQ);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss<KT>(tmem + kColS + 128 * w, qd + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
-                       kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), k > 0);
+            mma_ss(tmem + kColS + 128 * w, qd + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
+                   kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), idesc<KT>(), k > 0);
           if constexpr (TWO) {
             const uint64_t ld = desc_sw128(base + S::kLow + w * S::kTileQ);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              mma_ss<KT>(tmem + kColS + 128 * w, ld + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
-                         kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), 1u);
+              mma_ss(tmem + kColS + 128 * w, ld + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
+                     kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), idesc<KT>(), 1u);
           }
           commit(bar(S_FULL + w));
         }
@@ -607,13 +645,79 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
     } else {
       // ---- weights ----
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
-      const int w = warp >> 2;
+      const int w = warp >> 2, tr = tid & (kTileRows - 1);
       const uint32_t tmem_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * w;  // this warp's lanes
-      const float fac = row_fac[tid];
-      const int lim = row_lim[tid];
       const int my_take = w ? tile_take[1] : tile_take[0];
-      const uint32_t my_steps = w ? tile_steps[1] : tile_steps[0], my_items = w ? tile_items[1] : tile_items[0];
+      const uint32_t my_steps = w ? tile_steps[1] : tile_steps[0];
+      const uint32_t my_query = base + S::kQuery + w * S::kTileQ + tr * 128;
+      // this thread's row: turned, scaled by a power of two, fp16, back into the operand's place
+      float fac = 0.0f;
+      int lim = 0x7FFFFFFF;  // a row that is not there is not masked, and not used
+      if (turned) {
+        wait_bounded(bar(TURN + w), turns & 1u, abort_flag, a.status);
+        __syncwarp();
+        tc_fence_after();
+      }
+      if (w < tiles) {
+        auto get = [&](int c, float (&x)[32]) {  // coordinates 32 c .. 32 c + 31
+          if (turned) {
+            uint32_t v[32];
+            tmem_ld32(tmem_row + kColS + 32 * c, v);
+            wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float y[8];
+              unpack8<T>(lds128(my_query + (c >> 1) * (kTileRows * 128) + (((4 * (c & 1) + j) ^ (tr & 7)) << 4)), y);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) x[8 * j + q] = y[q];
+            }
+          }
+        };
+        float top = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float x[32];
+          get(c, x);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(x[j]));
+        }
+        const int e = min(max(scale_exp(top), -100), 120);
+        const float f = pow2(-e);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float x[32];
+          get(c, x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float y[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] = x[8 * j + q] * f;
+            const uint4 hi = pack8<__half>(y);
+            const uint32_t to = (c >> 1) * (kTileRows * 128) + (((4 * (c & 1) + j) ^ (tr & 7)) << 4);
+            sts128(my_query + to, hi.x, hi.y, hi.z, hi.w);
+            if constexpr (TWO) {
+              float z[8];
+              unpack8<__half>(hi, z);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) z[q] = y[q] - z[q];
+              const uint4 lo = pack8<__half>(z);
+              sts128(base + S::kLow + w * S::kTileQ + tr * 128 + to, lo.x, lo.y, lo.z, lo.w);
+            }
+          }
+        }
+        if (tid < rows) {
+          fac = pow2(e) * a.scale * (turned ? a.r.norm : 1.0f);
+          lim = a.causal ? s.len - s.n + row_token(a, qt * kRows + tid) + 1 : s.len;
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tc_fence_before();
+      asm volatile("bar.sync 1, 288;" ::: "memory");
       float top = 0.0f, sum = 0.0f;
       bool none = true;  // no key seen so far: the maximum says nothing
       for (int t = 0; t < my_take; ++t) {
@@ -669,90 +773,158 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(bar(P_FULL + 2 * w + hf));
         }
       }
-      if (my_take > 0) {
-        wait_bounded(bar(O_FULL + w), my_items & 1u, abort_flag, a.status);
-        __syncwarp();
-        tc_fence_after();
-      }
       row_stat[tid] = make_float2(none && sum == sum ? -INFINITY : top, sum);  // (a NaN query's piece counts)
     }
-    // The rows' sums go through shared memory, in the operands' place: both tiles are done.
-    __syncthreads();
+    // Both tiles are done: what the operands stood in is free.
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      if (tile_take[w] > 0) wait_bounded(bar(O_FULL + w), tile_items[w] & 1u, abort_flag, a.status);
+    __syncwarp();
+    tc_fence_after();
+    const bool whole_item = first && last;
+    float row_back = 1.0f;  // this thread's row's power of two in the turn back
+    turns += turned;
     if (warp < 8) {
-      const int w = warp >> 2;
+      const int w = warp >> 2, tr = tid & (kTileRows - 1);
       const uint32_t tmem_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * w;
+      const uint32_t my_query = base + S::kQuery + w * S::kTileQ + tr * 128;
+      const bool some = (w ? tile_take[1] : tile_take[0]) > 0;
+      if (whole_item && w < tiles) {
+        // the rows as operands of the turn back, in two terms, or as they are stored
+        const float y = row_stat[tid].y;
+        float f = (y > 0.0f ? 1.0f / y : y == 0.0f ? 0.0f : y) * (turned ? a.r.norm : 1.0f);
+        if (std::is_same<T, __half>::value && turned) {  // fp16 terms: beside a power of two, for their range
+          float top = 0.0f;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if ((w ? tile_take[1] : tile_take[0]) > 0) {
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem_row + kColO + c, o);
+            wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(__uint_as_float(o[j])));
+          }
+          const int e = min(max(scale_exp(top * f), -60), 60);
+          f *= pow2(-e), row_back = pow2(e);
+        }
+        const uint32_t my_low = base + (w ? S::kSumLow1 : S::kSumLow0) + tr * 128;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
           tmem_ld32(tmem_row + kColO + c, o);
           wait_ld();
-        } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
+          for (int j = 0; j < 4; ++j) {
+            float x[8], z[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = __uint_as_float(o[8 * j + q]) * f;
+            const uint4 hi = pack8<T>(x);
+            const uint32_t to = (c >> 6) * (kTileRows * 128) + (((((c >> 3) & 7) + j) ^ (tr & 7)) << 4);
+            sts128(my_query + to, hi.x, hi.y, hi.z, hi.w);
+            if (turned) {
+              unpack8<T>(hi, z);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) z[q] = x[q] - z[q];
+              const uint4 lo = pack8<T>(z);
+              sts128(my_low + to, lo.x, lo.y, lo.z, lo.w);
+            }
+          }
         }
+      } else if (!whole_item) {
+        // a piece: the rows' sums as they are, 16-byte chunks turned by the row
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tmem_row + kColO + c, o);
+          wait_ld();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          sts128(base + tid * (D * 4) + (((c / 4 + j) ^ (tid & 7)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t to = base + tid * (D * 4) + (((c / 4 + j) ^ (tid & 7)) << 4);
+            if (some)
+              sts128(to, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            else
+              sts128(to, 0u, 0u, 0u, 0u);
+          }
+        }
       }
-      tc_fence_before();
+    } else if (whole_item && turned) {
+      for (int c = tid - 256; c < D * LPR; c += 160) {
+        const uint4 w = turn_chunk<true>(inv, c / LPR, c % LPR, a.r.h, one);
+        sts128(base + S::kMatrix + ((c % LPR) >> 3) * (D * 128) + (c / LPR) * 128 + (((c & 7) ^ (c / LPR & 7)) << 4), w.x, w.y, w.z,
+               w.w);
+      }
     }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before();
     __syncthreads();
-    if (warp < 8) {
-      const LaneTurn turn = lane_turn(a.r, l);
-      T* turn_row = reinterpret_cast<T*>(sm + S::kTurnOut) + (tid / LPR) * D;
-      for (int p = 0; p < rows; p += BATCH * PASS) {
-        float x[BATCH][8];
-        float2 stat[BATCH];
+    tc_fence_after();
+    if (whole_item && turned) {
+      if (warp == 12) {
+        if (elect_one()) {
+          const uint64_t md = desc_sw128(base + S::kMatrix);
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          const int r = p + k * PASS + tid / LPR;
-          const float4 lo = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l) ^ (r & 7)) << 4));
-          const float4 hi = *reinterpret_cast<const float4*>(sm + r * (D * 4) + (((2 * l + 1) ^ (r & 7)) << 4));
-          x[k][0] = lo.x, x[k][1] = lo.y, x[k][2] = lo.z, x[k][3] = lo.w;
-          x[k][4] = hi.x, x[k][5] = hi.y, x[k][6] = hi.z, x[k][7] = hi.w;
-          stat[k] = row_stat[r];
+          for (int w = 0; w < 2; ++w) {
+            if (w < tiles) {
+#pragma unroll
+              for (int term = 0; term < 2; ++term) {
+                const uint64_t od = desc_sw128(base + (term == 0 ? S::kQuery + w * S::kTileQ : w ? S::kSumLow1 : S::kSumLow0));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                  mma_ss(tmem + kColS + 128 * w, od + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
+                         md + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), idesc_of<T, D>(), term > 0 || k > 0);
+              }
+            }
+            commit(bar(TURN + w));
+          }
         }
-        if (first && last) {
-          uint4 w[BATCH];
+        __syncwarp();
+      } else if (warp < 8) {
+        const int w = warp >> 2, tr = tid & (kTileRows - 1);
+        const uint32_t tmem_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * w;
+        const uint32_t my_query = base + S::kQuery + w * S::kTileQ + tr * 128;
+        wait_bounded(bar(TURN + w), turns & 1u, abort_flag, a.status);
+        __syncwarp();
+        tc_fence_after();
+        if (w < tiles) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem_row + kColS + c, o);
+            wait_ld();
 #pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const float y = stat[k].y, inv = y > 0.0f ? 1.0f / y : y == 0.0f ? 0.0f : y;
+            for (int j = 0; j < 4; ++j) {
+              float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[k][j] *= inv;
+              for (int q = 0; q < 8; ++q) x[q] = __uint_as_float(o[8 * j + q]) * row_back;
+              const uint4 hi = pack8<T>(x);
+              sts128(my_query + (c >> 6) * (kTileRows * 128) + (((((c >> 3) & 7) + j) ^ (tr & 7)) << 4), hi.x, hi.y, hi.z, hi.w);
+            }
           }
-          if (a.r.perm) {
-            unrotate_rows<T, BATCH, PASS * D>(x, turn, l, a.r, turn_row);
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) w[k] = *reinterpret_cast<const uint4*>(turn_row + k * PASS * D + 8 * l);
-            __syncwarp();
-          } else {
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) w[k] = pack8<T>(x[k]);
-          }
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const int r = p + k * PASS + tid / LPR, gr = qt * kRows + r, i = row_token(a, gr);
-            if (r < rows)
-              *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
-                                        ((long long)h * a.group + (gr - i * a.group)) * a.oh + 8 * l) = w[k];
-          }
+        }
+        tc_fence_before();
+      }
+      ++turns;
+      __syncthreads();
+    }
+    if (warp < 8) {
+#pragma unroll 4
+      for (int p = 0; p < rows; p += PASS) {
+        const int r = p + tid / LPR;
+        if (r >= rows) continue;
+        if (whole_item) {
+          const int tr = r & (kTileRows - 1), gr = qt * kRows + r, i = row_token(a, gr);
+          const uint4 w = lds128(base + S::kQuery + (r / kTileRows) * S::kTileQ + (l >> 3) * (kTileRows * 128) + tr * 128 +
+                                 (((l & 7) ^ (tr & 7)) << 4));
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
+                                    ((long long)h * a.group + (gr - i * a.group)) * a.oh + 8 * l) = w;
         } else {
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const int r = p + k * PASS + tid / LPR;
-            if (r >= rows) continue;
-            float4* o = reinterpret_cast<float4*>(a.piece + (slot + r) * D + 8 * l);
-            o[0] = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
-            o[1] = make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
-            if (l == 0) *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = stat[k];
-          }
+          uint4* o = reinterpret_cast<uint4*>(a.piece + (slot + r) * D + 8 * l);
+          o[0] = lds128(base + r * (D * 4) + (((2 * l) ^ (r & 7)) << 4));
+          o[1] = lds128(base + r * (D * 4) + (((2 * l + 1) ^ (r & 7)) << 4));
+          if (l == 0) *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = row_stat[r];
         }
       }
     }
     if (first && !last) desc = make_int4((int)((item_end - 1) / sh.size) - cta + 1, b, h, qt);
-    tc_fence_after();
     __syncthreads();
     steps += take;
 #pragma unroll

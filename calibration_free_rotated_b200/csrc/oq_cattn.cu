@@ -10,9 +10,9 @@
 // fp16, sums are fp32.
 //
 // The running maximum is taken over score + ev (logarithms to base 2), so the
-// weights p * 2^ev that go to fp16 are at most 2^8 and right to 2^-12 where they
+// weights p * 2^ev that go to fp16 are at most 2^15 and right to 2^-12 where they
 // matter, whatever the pages' scales; the softmax sum takes them back times
-// 2^-ev in fp32.  The maximum is raised only when a score passes it by 8: the
+// 2^-ev in fp32.  The maximum is raised only when a score passes it by 15: the
 // accumulators are rarely touched, and most tiles need no exchange at all.
 //
 // Tensor tiles m16n8k16 with the cache as the left operand: keys (tokens x D)
@@ -299,7 +299,7 @@ step_kernel(const __grid_constant__ Args a) {
             if (tok + g + 8 >= lim[n][j] || kscale == 0.0f) s1 = -INFINITY;
           }
           sc[n][j] = s0, sc[n][2 + j] = s1;
-          raise |= fmaxf(s0, s1) > top[n][j] + 8.0f;
+          raise |= fmaxf(s0, s1) > top[n][j] + kRaise;
         }
       if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll

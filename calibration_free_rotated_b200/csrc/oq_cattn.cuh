@@ -28,6 +28,10 @@ namespace cattn {
 
 using namespace cache;
 
+// A row's running maximum is raised when a weight would pass 2^15 (fp16 holds 65504):
+// the weights' relative rounding is the same anywhere below, and few steps then
+// have to rescale what is summed up.
+constexpr float kRaise = 15.0f;
 // Most CTAs that the workspace has pieces for (the kernels' residency on 148 SMs).
 constexpr int kStepCtas = 148 * 4, kChunkCtas = 148;
 

@@ -24,8 +24,8 @@
 //
 // Scales: as in oq_cattn.cu the running maximum is taken over score + ev, so
 // the weights carry their page's value exponent; groups of 16 tokens (no page is
-// smaller) have their own.  The accumulator is rescaled only when a row's maximum
-// has grown by more than 2^8.
+// smaller) have their own.  The accumulator is rescaled only when a weight would
+// pass 2^15.
 //
 // fp16 queries keep a second term: the turn rounds them to 2^-12, which would
 // show beside an fp16 result, so what the first operand leaves out goes into a
@@ -732,14 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const int left = lim - (tok0 + t * KT + HK * hf);  // keys of the half that the row may see
           const bool whole = __all_sync(0xFFFFFFFFu, left >= HK);
           // The weights at once, against the maximum so far; in the rare step that
-          // raises it (2^8 and more above, or the first keys of a row) once more
+          // raises it (2^15 and more above, or the first keys of a row) once more
           // from the scores, which still stand in TMEM.
           uint32_t p[HK / 2];
           for (int tries = 0; tries < 2; ++tries) {
             float mx;
             const float more = whole ? weigh<HK, false>(from, sc, fac, top, left, p, mx)
                                      : weigh<HK, true>(from, sc, fac, top, left, p, mx);
-            const bool raise = mx > 8.0f || (none && mx > -INFINITY);
+            const bool raise = mx > kRaise || (none && mx > -INFINITY);
             if (tries > 0 || !__any_sync(0xFFFFFFFFu, raise)) {
               sum += more;
               break;

@@ -378,48 +378,60 @@ class KVCache:
         self._ref = ctypes.byref(self._struct)
 
 
+# The calls below cost a few microseconds on the host, which is what small launches
+# are paced by: checks look at each tensor once, and the current device and
+# stream come from the raw getters that torch.cuda's own objects are made from.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _launch(fn, device, stream, *args):
     """fn(*args, stream) with the tensors' device current."""
+    index = device.index
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device (got {device})")
-    if device.index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            rc = fn(*args, s.cuda_stream)
+            rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
-        rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc)
 
 
-def _rows(name, t, heads=None, d=None, like=None):
-    """Strides (token, head) of [T, heads, d] rows; checks what the library cannot see."""
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (d is not None and t.shape[2] != d):
-        raise ValueError(f"{name} must be [T, {heads or 'heads'}, {d or 'd'}] (got {tuple(t.shape)})")
-    st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
+def _rows(name, t, heads, d):
+    """Strides (token, head) of [T, heads, d] rows and the dtype's code; checks
+    what the library cannot see (heads, d: None for any)."""
+    shape, strides, dtype = t.shape, t.stride(), DTYPES.get(t.dtype)
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (d is not None and shape[2] != d):
+        raise ValueError(f"{name} must be [T, {heads or 'heads'}, {d or 'd'}] (got {tuple(shape)})")
+    if strides[2] != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if like is not None and (t.shape[0] != like.shape[0] or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must match in tokens, dtype and device (got {tuple(t.shape)}, {t.dtype}, {t.device})")
-    if t.dtype not in DTYPES:
+    if dtype is None:
         raise ValueError(f"{name}: dtype {t.dtype} is not supported")
-    return st, sh
+    return strides[0], strides[1], dtype
+
+
+def _alike(name, t, like):
+    if t.shape[0] != like.shape[0] or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must match in tokens, dtype and device (got {tuple(t.shape)}, {t.dtype}, {t.device})")
 
 
 def _index(name, t, device, shape):
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or \
-            (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be contiguous int32{'' if shape is None else ' ' + str(list(shape))} on {device} "
-                         f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {device} "
+                         f"(got {t.dtype} {list(t.shape)} on {t.device})")
     return t.data_ptr()
 
 
-def _batch(cache, cu, at_name, at, table):
-    if at.dim() != 1 or table.dim() != 2 or table.shape[0] != at.shape[0]:
+def _batch(device, cu, at_name, at, table):
+    """Pointers of a batch's index tensors, and B and the table's width."""
+    if at.dim() != 1 or table.dim() != 2:
         raise ValueError(f"{at_name} must be [B] and table [B, width] (got {tuple(at.shape)}, {tuple(table.shape)})")
-    B, dev = at.shape[0], cache.device
-    return (_index("cu", cu, dev, (B + 1,)), _index(at_name, at, dev, None), B, _index("table", table, dev, None),
-            table.shape[1])
+    B, width = at.shape[0], table.shape[1]
+    return (_index("cu", cu, device, (B + 1,)), _index(at_name, at, device, (B,)), B,
+            _index("table", table, device, (B, width)), width)
 
 
 def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out=None, inverse: bool = False, stream=None):
@@ -427,13 +439,17 @@ def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out=None, inverse
     tokens and heads) turned by pos: int32 [T, axes].  out: written and returned
     (x itself: in place); a new tensor if None.  inverse: the transposed turn,
     which is also the gradient."""
-    xt, xh = _rows("x", x)
+    xt, xh, code = _rows("x", x, None, None)
     T, heads, d = x.shape
     if out is None:
         out = torch.empty((T, heads, d), dtype=x.dtype, device=x.device)
-    ot, oh = _rows("out", out, heads, d, like=x)
-    _launch(_lib.oq_rope_apply, x.device, stream, rope.handle, x.data_ptr(), xt, xh, out.data_ptr(), ot, oh,
-            DTYPES[x.dtype], T, heads, d, _index("pos", pos, x.device, (T, rope.n_axes)), inverse)
+        ot, oh = heads * d, d
+    else:
+        ot, oh, _ = _rows("out", out, heads, d)
+        _alike("out", out, x)
+    device = x.device
+    _launch(_lib.oq_rope_apply, device, stream, rope._h, x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, code, T, heads, d,
+            _index("pos", pos, device, (T, rope.n_axes)), inverse)
     return out
 
 
@@ -442,13 +458,15 @@ def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tens
     """Quantizes the rows k, v (cuda bf16 / fp16 [T, heads, d], rows cu[b] ..
     cu[b+1]-1 are sequence b's) into the cache behind the past[b] tokens that
     the sequence holds, in the pages of table: int32 [B, width]."""
-    kt, kh = _rows("k", k, cache.heads, cache.d)
-    vt, vh = _rows("v", v, cache.heads, cache.d, like=k)
-    if k.device != cache.device:
-        raise ValueError(f"k and v must be on the cache's device {cache.device}")
-    cu_p, at_p, B, table_p, width = _batch(cache, cu, "past", past, table)
-    _launch(_lib.oq_cache_write, cache.device, stream, cache._ref, None if rpbh is None else rpbh.handle, k.data_ptr(),
-            kt, kh, v.data_ptr(), vt, vh, DTYPES[k.dtype], k.shape[0], cu_p, at_p, B, table_p, width)
+    kt, kh, code = _rows("k", k, cache.heads, cache.d)
+    vt, vh, _ = _rows("v", v, cache.heads, cache.d)
+    _alike("v", v, k)
+    device = cache.device
+    if k.device != device:
+        raise ValueError(f"k and v must be on the cache's device {device}")
+    cu_p, at_p, B, table_p, width = _batch(device, cu, "past", past, table)
+    _launch(_lib.oq_cache_write, device, stream, cache._ref, None if rpbh is None else rpbh._h, k.data_ptr(), kt, kh,
+            v.data_ptr(), vt, vh, code, k.shape[0], cu_p, at_p, B, table_p, width)
 
 
 def cache_read(cache: KVCache, cu: torch.Tensor, first: torch.Tensor, table: torch.Tensor, T: int = None,
@@ -458,15 +476,17 @@ def cache_read(cache: KVCache, cu: torch.Tensor, first: torch.Tensor, table: tor
     passed, with T rows)."""
     if (k is None) != (v is None) or (k is None and T is None):
         raise ValueError("pass k and v, or T")
+    device = cache.device
     if k is None:
-        k, v = (torch.empty((T, cache.heads, cache.d), dtype=dtype, device=cache.device) for _ in range(2))
-    _rows("k", k, cache.heads, cache.d)
-    _rows("v", v, cache.heads, cache.d, like=k)
-    if not k.is_contiguous() or not v.is_contiguous() or k.device != cache.device or (T is not None and T != k.shape[0]):
+        k, v = (torch.empty((T, cache.heads, cache.d), dtype=dtype, device=device) for _ in range(2))
+    _, _, code = _rows("k", k, cache.heads, cache.d)
+    _rows("v", v, cache.heads, cache.d)
+    _alike("v", v, k)
+    if not k.is_contiguous() or not v.is_contiguous() or k.device != device or (T is not None and T != k.shape[0]):
         raise ValueError("k and v must be contiguous, of T rows, on the cache's device")
-    cu_p, at_p, B, table_p, width = _batch(cache, cu, "first", first, table)
-    _launch(_lib.oq_cache_read, cache.device, stream, cache._ref, None if rpbh is None else rpbh.handle, k.data_ptr(),
-            v.data_ptr(), DTYPES[k.dtype], k.shape[0], cu_p, at_p, B, table_p, width)
+    cu_p, at_p, B, table_p, width = _batch(device, cu, "first", first, table)
+    _launch(_lib.oq_cache_read, device, stream, cache._ref, None if rpbh is None else rpbh._h, k.data_ptr(),
+            v.data_ptr(), code, k.shape[0], cu_p, at_p, B, table_p, width)
     return k, v
 
 
@@ -480,21 +500,24 @@ def cache_attention(cache: KVCache, q: torch.Tensor, cu: torch.Tensor, lens: tor
     """Attention of the rows q (cuda bf16 / fp16 [T, heads, d], rows cu[b] ..
     cu[b+1]-1 are sequence b's newest tokens) over the lens[b] tokens that the
     sequence holds in the cache, these among them.  scale: 1/sqrt(d) if None."""
-    qt, qh = _rows("q", q, None, cache.d)
+    qt, qh, code = _rows("q", q, None, cache.d)
     T, heads, d = q.shape
-    if q.device != cache.device:
-        raise ValueError(f"q must be on the cache's device {cache.device}")
+    device = cache.device
+    if q.device != device:
+        raise ValueError(f"q must be on the cache's device {device}")
     if out is None:
-        out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
-    ot, oh = _rows("out", out, heads, d, like=q)
-    cu_p, at_p, B, table_p, width = _batch(cache, cu, "lens", lens, table)
+        out = torch.empty((T, heads, d), dtype=q.dtype, device=device)
+        ot, oh = heads * d, d
+    else:
+        ot, oh, _ = _rows("out", out, heads, d)
+        _alike("out", out, q)
+    cu_p, at_p, B, table_p, width = _batch(device, cu, "lens", lens, table)
     if workspace is None:
         need = _lib.oq_cache_attention_workspace_bytes(cache._ref, T, B, heads)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on q's device")
-    _launch(_lib.oq_cache_attention, cache.device, stream, cache._ref, None if rpbh is None else rpbh.handle,
-            q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, DTYPES[q.dtype], heads, T, cu_p, at_p, B, table_p, width,
-            causal, d ** -0.5 if scale is None else scale, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+    _launch(_lib.oq_cache_attention, device, stream, cache._ref, None if rpbh is None else rpbh._h, q.data_ptr(), qt, qh,
+            out.data_ptr(), ot, oh, code, heads, T, cu_p, at_p, B, table_p, width, causal,
+            d ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.nbytes)
     return out

@@ -11,13 +11,25 @@
 // portions the tokens came.  Powers of two make code * 2^e exact in bf16 and
 // fp16 products, and the requantising exact integer work.
 //
-// Writing: a CTA takes one page, one head, keys or values.  Its rows' rotated
-// values stay in registers between the two steps (the maximum, then the codes),
-// so each input is read once.  Reading back: a CTA takes some rows of one head.
-// Both are bound by memory for chunks and by latency for single tokens.
+// Both directions are bound by memory for chunks and by latency for single tokens,
+// if the turn costs little.  A warp turns 16 rows: half of the Hadamard transform
+// (over four of a coordinate's bits) is a product with a 16 x 16 matrix of signs on
+// the tensor cores (m16n8k16; the inputs are 16-bit values or codes, the entries 1,
+// -1 and 0, the sums fp32: as exact as additions), the other bits are butterflies
+// between accumulators.  Which bits: a lane's 16-byte piece of a row of codes is
+// coordinates 64 j + 16 c + 4 w + e (c = lane % 4); the product of step (j, w) takes
+// e and c together (bits 0, 1, 4, 5), so w and j (bits 2, 3, 6) stay between the
+// lane's own accumulators, and it ends with the same 16 coordinates of the turned
+// row: codes are read and written as they lie.  (With eight coordinates a lane and
+// butterflies by shuffles, four times as many instructions, the write took 54 us and
+// the read 42 us for 4608 tokens of 24 heads.)
+//
+// The permutation goes through shared memory on the 16-bit side, in 32-bit words of
+// two rows (g and g + 8, as the product's operands and results have them).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "oq_cache.cuh"
 
@@ -26,7 +38,101 @@ namespace {
 
 using namespace cache;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the read kernel
+
+__device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long f2_sub(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long f2(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_split(unsigned long long v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                        uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Two of four codes (bytes, sign bits turned) as fp16: see oq_cattn.cuh.
+__device__ __forceinline__ uint32_t code_pair(uint32_t biased, uint32_t sel) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(biased, 0x64646464u, sel)), "r"(0x64806480u));
+  return r;
+}
+
+// The 16 x 16 matrix of signs as two right operands (results e = 0, 1 and e = 2, 3):
+// slot k of lane c stands for the coordinate bits (e, c), column n = 2 c' + b for
+// (b + 2 tile, c').  Blocks of 32 leave bit 5 alone: entries between its halves are 0.
+template <typename T>
+__device__ __forceinline__ void sign_matrix(uint32_t (&m)[2][2], int lane, int h) {
+  const int g = lane >> 2, c = lane & 3, c2 = g >> 1, b = g & 1;
+  const uint32_t one = std::is_same<T, __nv_bfloat16>::value ? 0x3F80u : 0x3C00u;
+  const bool zero = h == 32 && ((c ^ c2) & 2);
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {  // slots 2 c, 2 c + 1: e = 0, 1; slots + 8: e = 2, 3
+      uint32_t w = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t odd = (uint32_t)(__popc(c & (h == 32 ? 1 : 3) & c2) + (u & b) + (r & t)) & 1u;
+        w |= (one | odd << 15) << (16 * u);
+      }
+      m[t][r] = zero ? 0u : w;
+    }
+}
+
+// The butterflies over bits 2, 3 and (blocks of 128) 6.
+template <int KS>
+__device__ __forceinline__ void butterflies(float (&acc)[KS][2][4], int h) {
+#pragma unroll
+  for (int s = 1; s < KS; s <<= 1) {
+    if (s == 4 && h < 128) break;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      if (!(k & s)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const unsigned long long a = f2(acc[k][t][i], acc[k][t][i + 1]);
+            const unsigned long long b = f2(acc[k + s][t][i], acc[k + s][t][i + 1]);
+            f2_split(f2_add(a, b), acc[k][t][i], acc[k][t][i + 1]);
+            f2_split(f2_sub(a, b), acc[k + s][t][i], acc[k + s][t][i + 1]);
+          }
+      }
+  }
+}
 
 struct WriteArgs {
   View c;
@@ -38,148 +144,231 @@ struct WriteArgs {
   const int* past;
   const int* table;
   int* status;
-  int B, T, width;
+  int B, T, width, units;
 };
 
-// Finds the unit-th page that the sequences' new tokens touch.  All threads
-// return the same answer; seq = -1 when there are fewer.
+// The unit-th page that the sequences' new tokens touch; seq = -1 when there are
+// fewer.  Each warp looks for itself.
 struct Place {
-  int seq, slot;   // sequence and the page's index in its table row
+  int seq, slot;  // sequence and the page's index in its table row
   int cu0, past, n;
 };
-__device__ Place find_place(const WriteArgs& a, int unit, bool report) {
-  __shared__ int warp_sum[kThreads / 32];
-  __shared__ Place found;
-  if (threadIdx.x == 0) found.seq = -1;
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ Place find_place(const WriteArgs& a, int unit, bool report) {
+  const int lane = threadIdx.x & 31;
+  Place at;
+  at.seq = -1, at.slot = 0, at.cu0 = 0, at.past = 0, at.n = 0;
   int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    int cu0 = 0, n = 0, past = 0, pages = 0;
-    if (b < a.B) {
-      cu0 = a.cu[b];
-      const int cu1 = a.cu[b + 1];
-      past = a.past[b];
-      // a row of the batch whose numbers do not fit is left out, and reported
-      const bool ok = cu0 >= 0 && cu1 >= cu0 && cu1 <= a.T && past >= 0 &&
-                      (long long)past + (cu1 - cu0) <= (long long)a.width * a.c.page;
-      n = ok ? cu1 - cu0 : 0;
-      if (!ok && report) bad_index(a.status);
-      if (n > 0) pages = (past + n - 1) / a.c.page - past / a.c.page + 1;
-    }
-    int incl = pages;
+  for (int b0 = 0; b0 < a.B; b0 += 128) {
+    int cu0[4], cu1[4], past[4];  // four groups of 32 sequences: their loads together
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-      if (lane >= m) incl += o;
+    for (int q = 0; q < 4; ++q) {
+      const int b = b0 + 32 * q + lane;
+      const bool in = b < a.B;
+      cu0[q] = in ? a.cu[b] : 0, cu1[q] = in ? a.cu[b + 1] : 0, past[q] = in ? a.past[b] : 0;
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int base = before, all = before;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) base += warp_sum[w];
-      all += warp_sum[w];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // a row of the batch whose numbers do not fit is left out, and reported
+      const bool ok = cu0[q] >= 0 && cu1[q] >= cu0[q] && cu1[q] <= a.T && past[q] >= 0 &&
+                      (long long)past[q] + (cu1[q] - cu0[q]) <= (long long)a.width * a.c.page;
+      const int n = ok ? cu1[q] - cu0[q] : 0;
+      if (!ok && report) bad_index(a.status);
+      const int pages = n > 0 ? (past[q] + n - 1) / a.c.page - past[q] / a.c.page + 1 : 0;
+      int incl = pages;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+        if (lane >= m) incl += o;
+      }
+      const int first = before + incl - pages;
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, unit >= first && unit < first + pages);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        at.seq = b0 + 32 * q + src;
+        at.cu0 = __shfl_sync(0xFFFFFFFFu, cu0[q], src);
+        at.past = __shfl_sync(0xFFFFFFFFu, past[q], src);
+        at.n = __shfl_sync(0xFFFFFFFFu, n, src);
+        at.slot = at.past / a.c.page + (unit - __shfl_sync(0xFFFFFFFFu, first, src));
+      }
+      before += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    const int first = base + incl - pages;
-    if (unit >= first && unit < first + pages) {
-      found.seq = b;
-      found.slot = past / a.c.page + (unit - first);
-      found.cu0 = cu0, found.past = past, found.n = n;
-    }
-    __syncthreads();
-    before = all;
-    if (unit < all && !report) break;  // the same for all threads
+    if (unit < before && !report) break;
   }
-  return found;
+  return at;
 }
 
-template <typename T, int D, int PASSES>
-__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ WriteArgs a) {
-  constexpr int LPR = D / 8;               // lanes of a row
-  constexpr int ROWS = kThreads / LPR;     // rows of a pass
-  __shared__ __align__(16) T stage[ROWS][D];
-  __shared__ float warp_max[kThreads / 32];
+// WPU warps (one for every 16 tokens) write a page's rows of one head, keys or values.
+template <typename T, int D, int WPU>
+__global__ void __launch_bounds__(WPU < 4 ? 128 : 32 * WPU) write_kernel(const __grid_constant__ WriteArgs a) {
+  constexpr int WARPS = WPU < 4 ? 4 : WPU, UNITS = WARPS / WPU, P = 16 * WPU;
+  constexpr int KS = D / 16, PITCH = D + 4;  // words of a row pair in shared memory
+  __shared__ __align__(16) uint32_t stage[WARPS][8 * PITCH];
+  __shared__ uint32_t warp_top[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int unit = blockIdx.x * UNITS + warp / WPU, row0 = 16 * (warp % WPU);
   const int head = blockIdx.y;
   const bool values = blockIdx.z != 0;
-  const Place at = find_place(a, blockIdx.x, blockIdx.y == 0 && blockIdx.z == 0 && blockIdx.x == 0);
-  if (at.seq < 0) return;
-  const int page = a.table[(size_t)at.seq * a.width + at.slot];
-  if (page < 0 || page >= a.c.n_pages) {
-    if (threadIdx.x == 0) bad_index(a.status);
-    return;
+  Place at = find_place(a, unit, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0);
+  int page = 0;
+  if (at.seq >= 0) {
+    page = a.table[(size_t)at.seq * a.width + at.slot];
+    if (page < 0 || page >= a.c.n_pages) {
+      if (lane == 0) bad_index(a.status);
+      at.seq = -1;
+      page = 0;
+    }
   }
-  const int P = a.c.page;
-  const int start = at.slot * P;                        // position of the page's first token
-  const int held = min(max(at.past - start, 0), P);     // tokens it holds already
-  const int end = min(at.past + at.n - start, P);       // and after this call
-  const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
-  const T* src = static_cast<const T*>(values ? a.v : a.k) + head * (values ? a.vh : a.kh) + 8 * l;
+  const int start = at.slot * P;                                            // position of the page's first token
+  const int held = at.seq < 0 ? 0 : min(max(at.past - start, 0), P);        // tokens it holds already
+  const int end = at.seq < 0 ? 0 : min(at.past + at.n - start, P);          // and after this call
+  const T* src = static_cast<const T*>(values ? a.v : a.k) + head * (values ? a.vh : a.kh);
   const long long stride = values ? a.vt : a.kt;
   const long long first = (long long)at.cu0 + start - at.past;  // input row of the page's place 0
-  const LaneTurn turn = lane_turn(a.r, l);
-
-  float u[PASSES][8];
-  float top = 0.0f;
-#pragma unroll
-  for (int q = 0; q < PASSES; ++q) {
-    const int row = held + q * ROWS + r0;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (row < end) w = *reinterpret_cast<const uint4*>(src + (first + row) * stride);
-    if (a.r.perm) {
-      *reinterpret_cast<uint4*>(&stage[r0][8 * l]) = w;
-      __syncwarp();
-      rotate_row<T>(stage[r0], turn, l, a.r, u[q]);
-      __syncwarp();
-    } else {
-      unpack8<T>(w, u[q]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(u[q][i]));
-  }
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
   float* scale = (values ? a.c.vs : a.c.ks) + (size_t)page * a.c.heads + head;
   const int e_old = held > 0 ? min(max(scale_exp(*scale), kExpMin), kExpMax) : kExpMin;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, warp_max[w]);
-  const int e = max(step_exp(top), e_old);
-  int8_t* dst = (values ? a.c.v : a.c.k) + ((size_t)page * a.c.heads + head) * P * D;
+  const bool some = row0 < end && row0 + 16 > held;  // whether this warp has rows: the same for the warp
 
-  if (held > 0 && e > e_old) {  // the same for all threads
-    const float f = pow2(e_old - e);
-    for (int i = threadIdx.x; i < held * (D / 4); i += kThreads) {
-      char4 c = reinterpret_cast<char4*>(dst)[i];
-      c.x = (signed char)__float2int_rn((float)c.x * f);
-      c.y = (signed char)__float2int_rn((float)c.y * f);
-      c.z = (signed char)__float2int_rn((float)c.z * f);
-      c.w = (signed char)__float2int_rn((float)c.w * f);
-      reinterpret_cast<char4*>(dst)[i] = c;
+  // acc[4 j + w][t][i]: row g (i < 2) or g + 8, coordinate 64 j + 16 c + 4 w + 2 t + i % 2
+  float acc[KS][2][4];
+#pragma unroll
+  for (int k = 0; k < KS; ++k)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[k][t][i] = 0.0f;
+  if (some) {
+    if (a.r.perm) {
+      uint32_t* st = stage[warp];
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        const int id = lane + 32 * q, r = id / (D / 8), ch = id % (D / 8);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+        const int lo = row0 + r, hi = lo + 8;
+        if (lo >= held && lo < end) x = *reinterpret_cast<const uint4*>(src + (first + lo) * stride + 8 * ch);
+        if (hi >= held && hi < end) y = *reinterpret_cast<const uint4*>(src + (first + hi) * stride + 8 * ch);
+        uint4* to = reinterpret_cast<uint4*>(st + r * PITCH + 8 * ch);
+        to[0] = make_uint4(__byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), __byte_perm(x.y, y.y, 0x5410),
+                           __byte_perm(x.y, y.y, 0x7632));
+        to[1] = make_uint4(__byte_perm(x.z, y.z, 0x5410), __byte_perm(x.z, y.z, 0x7632), __byte_perm(x.w, y.w, 0x5410),
+                           __byte_perm(x.w, y.w, 0x7632));
+      }
+      uint32_t m[2][2];
+      sign_matrix<T>(m, lane, a.r.h);
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const uint4* pi = reinterpret_cast<const uint4*>(a.r.perm + 64 * j + 16 * c);
+        const uint4 p0 = pi[0], p1 = pi[1];
+        const uint32_t at16[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+        const uint32_t neg = a.r.signs[2 * j + (c >> 1)] >> (16 * (c & 1));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t lo[2], hi[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {  // e = 2 u, 2 u + 1
+            const uint32_t p = at16[2 * w + u];
+            const uint32_t w0 = st[g * PITCH + (p & 0xFFFFu)], w1 = st[g * PITCH + (p >> 16)];
+            const uint32_t s2 = (neg >> (4 * w + 2 * u) & 1u) << 15 | (neg >> (4 * w + 2 * u + 1) & 1u) << 31;
+            lo[u] = __byte_perm(w0, w1, 0x5410) ^ s2;
+            hi[u] = __byte_perm(w0, w1, 0x7632) ^ s2;
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) mma16816<T>(acc[4 * j + w][t], lo[0], hi[0], lo[1], hi[1], m[t][0], m[t][1]);
+        }
+      }
+      butterflies<KS>(acc, a.r.h);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = row0 + g + 8 * r;
+        if (row >= held && row < end) {
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float x[8];
+              unpack8<T>(*reinterpret_cast<const uint4*>(src + (first + row) * stride + 64 * j + 16 * c + 8 * u), x);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) acc[4 * j + 2 * u + (i >> 2)][(i >> 1) & 1][2 * r + (i & 1)] = x[i];
+            }
+        }
+      }
     }
   }
-  const float inv = pow2(-e);
+  // the largest magnitude; NaN counts as 0
+  float top = 0.0f;
 #pragma unroll
-  for (int q = 0; q < PASSES; ++q) {
-    const int row = held + q * ROWS + r0;
-    if (row < end) {
-      uint32_t w[2];
+  for (int k = 0; k < KS; ++k)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        int c[4];
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max_nan(top, fabsf(acc[k][t][i]));
+  if (!(top == top)) {
+    top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float x = u[q][4 * j + i];
-          c[i] = __float2int_rn(fminf(fmaxf(x * inv, -127.0f), 127.0f));
-          if (!(x == x)) c[i] = 0;
+          float& x = acc[k][t][i];
+          if (!(x == x)) x = 0.0f;
+          top = fmaxf(top, fabsf(x));
         }
-        w[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-      }
-      *reinterpret_cast<uint2*>(dst + (size_t)row * D + 8 * l) = make_uint2(w[0], w[1]);
+  }
+  const uint32_t warp_most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+  if (lane == 0) warp_top[warp] = warp_most;
+  __syncthreads();  // (the page's old scale was read before)
+  uint32_t most = 0;
+#pragma unroll
+  for (int w = 0; w < WPU; ++w) most = max(most, warp_top[warp / WPU * WPU + w]);
+  const float norm = a.r.perm ? a.r.norm : 1.0f;
+  const float amax = __uint_as_float(most) * norm;
+  const int e = max(step_exp(amax), e_old);
+  int8_t* dst = (values ? a.c.v : a.c.k) + ((size_t)page * a.c.heads + head) * P * D;
+
+  if (held > 0 && e > e_old && end > 0) {  // the same for the page's warps
+    const float f = pow2(e_old - e);
+    for (int i = lane + 32 * (warp % WPU); i < held * (D / 4); i += 32 * WPU) {
+      char4 v = reinterpret_cast<char4*>(dst)[i];
+      v.x = (signed char)__float2int_rn((float)v.x * f);
+      v.y = (signed char)__float2int_rn((float)v.y * f);
+      v.z = (signed char)__float2int_rn((float)v.z * f);
+      v.w = (signed char)__float2int_rn((float)v.w * f);
+      reinterpret_cast<char4*>(dst)[i] = v;
     }
   }
-  if (threadIdx.x == 0) *scale = pow2(e);  // read by this CTA alone, before the barrier above
+  if (some) {
+    // rne(u / 2^e) as the low byte of a sum with 1.5 * 2^23: one rounding, of the exact product
+    const float to = norm * pow2(-e);
+    if (amax > 127.0f * pow2(kExpMax)) {  // saturates
+      const float lim = 127.0f * pow2(e) / norm;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[k][t][i] = fminf(fmaxf(acc[k][t][i], -lim), lim);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + g + 8 * r;
+      const bool mine = row >= held && row < end;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        uint32_t o[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(fmaf(acc[4 * j + w][i >> 1][2 * r + (i & 1)], to, 12582912.0f));
+          o[w] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
+        }
+        if (mine) *reinterpret_cast<uint4*>(dst + (size_t)row * D + 64 * j + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  if (end > 0 && lane == 0 && warp % WPU == 0) *scale = pow2(e);
 }
 
 struct ReadArgs {
@@ -191,73 +380,145 @@ struct ReadArgs {
   const int* first;
   const int* table;
   int* status;
-  int B, T, width;
+  int B, T, width, heads_warp;
 };
 
+// A warp reads 16 output rows of heads_warp heads, keys or values.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a, int rows_cta) {
-  constexpr int LPR = D / 8;
-  constexpr int ROWS = kThreads / LPR;
-  __shared__ __align__(16) T stage[ROWS][D];
-  __shared__ int place[128];  // row of codes (page * page size + place), or -1
-  const int head = blockIdx.y;
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int KS = D / 16, PITCH = D + 4;
+  __shared__ __align__(16) uint32_t stage[kThreads / 32][8 * PITCH];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int t0 = (blockIdx.x * (kThreads / 32) + warp) * 16;
+  if (t0 >= a.T) return;  // (no barrier of the CTA below)
   const bool values = blockIdx.z != 0;
-  const int t0 = blockIdx.x * rows_cta, nt = min(rows_cta, a.T - t0);
-  // the sequence of the CTA's first row: how many end at or before it
+  // the sequence of the warp's first row: how many end at or before it
   int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    before += __syncthreads_count(b < a.B && a.cu[b + 1] <= t0);
+  for (int b0 = 0; b0 < a.B; b0 += 128) {
+    int e[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int b = b0 + 32 * q + lane;
+      e[q] = b < a.B ? a.cu[b + 1] : 0x7FFFFFFF;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) before += __popc(__ballot_sync(0xFFFFFFFFu, e[q] <= t0));
   }
-  if (threadIdx.x < nt) {
-    const int t = t0 + threadIdx.x;
+  // row of codes (page * page size + place) of the lane's row, or -1; lanes 16.. stand for nothing
+  int at = -1;
+  if (lane < 16 && t0 + lane < a.T) {
+    const int t = t0 + lane;
     int b = before;
     while (b < a.B && a.cu[b + 1] <= t) ++b;
-    int at = -1;
     if (b < a.B && t >= a.cu[b]) {
       const long long p = (long long)a.first[b] + (t - a.cu[b]);
       if (p >= 0 && p < (long long)a.width * a.c.page) {
         const int page = a.table[(size_t)b * a.width + (int)(p / a.c.page)];
-        if (page >= 0 && page < a.c.n_pages) at = page;
-        if (at >= 0) place[threadIdx.x] = (int)(p % a.c.page);
+        if (page >= 0 && page < a.c.n_pages) at = page * a.c.page + (int)(p % a.c.page);
       }
       if (at < 0) bad_index(a.status);
     }
-    place[threadIdx.x] = at < 0 ? -1 : at * a.c.page + place[threadIdx.x];
   }
-  __syncthreads();
-  const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+  const int at0 = __shfl_sync(0xFFFFFFFFu, at, g), at1 = __shfl_sync(0xFFFFFFFFu, at, g + 8);
   const int8_t* codes = values ? a.c.v : a.c.k;
   const float* scales = values ? a.c.vs : a.c.ks;
   T* out = static_cast<T*>(values ? a.v : a.k);
-  const LaneTurn turn = lane_turn(a.r, l);
-  for (int q = 0; q < nt; q += ROWS) {
-    const int row = q + r0;
-    const int at = row < nt ? place[row] : -1;
-    uint2 w = make_uint2(0u, 0u);
-    float scale = 0.0f;
-    if (at >= 0) {
-      const int page = at / a.c.page, off = at - page * a.c.page;
-      const size_t ph = (size_t)page * a.c.heads + head;
-      w = *reinterpret_cast<const uint2*>(codes + (ph * a.c.page + off) * D + 8 * l);
-      scale = scales[ph];
-    }
-    float x[8];
+  const int plog = 31 - __clz(a.c.page);
+  const int h0 = blockIdx.y * a.heads_warp, h1 = min(h0 + a.heads_warp, a.c.heads);
+  uint32_t m[2][2];
+  sign_matrix<__half>(m, lane, a.r.h);
+
+  for (int h = h0; h < h1; ++h) {
+    uint4 w0[D / 64], w1[D / 64];
+    float f0 = 0.0f, f1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t word = i < 4 ? w.x : w.y;
-      x[i] = (float)(int)(signed char)(word >> (8 * (i & 3))) * scale;
+    for (int j = 0; j < D / 64; ++j) w0[j] = w1[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (at0 >= 0) {
+      const size_t ph = (size_t)(at0 >> plog) * a.c.heads + h;
+      f0 = scales[ph];
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+        w0[j] = *reinterpret_cast<const uint4*>(codes + ((ph << plog) + (at0 & (a.c.page - 1))) * D + 64 * j + 16 * c);
     }
-    uint4 o;
+    if (at1 >= 0) {
+      const size_t ph = (size_t)(at1 >> plog) * a.c.heads + h;
+      f1 = scales[ph];
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+        w1[j] = *reinterpret_cast<const uint4*>(codes + ((ph << plog) + (at1 & (a.c.page - 1))) * D + 64 * j + 16 * c);
+    }
     if (a.r.perm) {
-      unrotate_row<T>(x, turn, l, a.r, stage[r0]);
+      float acc[KS][2][4];
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const uint32_t x[4] = {w0[j].x, w0[j].y, w0[j].z, w0[j].w}, y[4] = {w1[j].x, w1[j].y, w1[j].z, w1[j].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t x8 = x[w] ^ 0x80808080u, y8 = y[w] ^ 0x80808080u;
+          const uint32_t a0 = code_pair(x8, 0x4140), a1 = code_pair(y8, 0x4140), a2 = code_pair(x8, 0x4342),
+                         a3 = code_pair(y8, 0x4342);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[4 * j + w][t][i] = 0.0f;
+            mma16816<__half>(acc[4 * j + w][t], a0, a1, a2, a3, m[t][0], m[t][1]);
+          }
+        }
+      }
+      butterflies<KS>(acc, a.r.h);
+      f0 *= a.r.norm, f1 *= a.r.norm;
+      uint32_t* st = stage[warp];
       __syncwarp();
-      o = *reinterpret_cast<const uint4*>(&stage[r0][8 * l]);
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const uint4* pi = reinterpret_cast<const uint4*>(a.r.perm + 64 * j + 16 * c);
+        const uint4 p0 = pi[0], p1 = pi[1];
+        const uint32_t at16[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+        const uint32_t neg = a.r.signs[2 * j + (c >> 1)] >> (16 * (c & 1));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float* v = acc[4 * j + (i >> 2)][(i >> 1) & 1];
+          const uint32_t pair = pack2<T>(v[i & 1] * f0, v[2 + (i & 1)] * f1);
+          const uint32_t p = (i & 1) ? at16[i >> 1] >> 16 : at16[i >> 1] & 0xFFFFu;
+          st[g * PITCH + p] = pair ^ ((neg >> i & 1u) ? 0x80008000u : 0u);
+        }
+      }
       __syncwarp();
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        const int id = lane + 32 * q, r = id / (D / 8), ch = id % (D / 8);
+        const uint4* from = reinterpret_cast<const uint4*>(st + r * PITCH + 8 * ch);
+        const uint4 x = from[0], y = from[1];
+        const int lo = __shfl_sync(0xFFFFFFFFu, at, r), hi = __shfl_sync(0xFFFFFFFFu, at, r + 8);
+        T* to = out + ((size_t)(t0 + r) * a.c.heads + h) * D + 8 * ch;
+        if (lo >= 0)
+          *reinterpret_cast<uint4*>(to) = make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
+                                                     __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
+        if (hi >= 0)
+          *reinterpret_cast<uint4*>(to + (size_t)8 * a.c.heads * D) =
+              make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632), __byte_perm(y.x, y.y, 0x7632),
+                         __byte_perm(y.z, y.w, 0x7632));
+      }
     } else {
-      o = pack8<T>(x);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if ((r ? at1 : at0) < 0) continue;
+        const float f = r ? f1 : f0;
+        T* to = out + ((size_t)(t0 + g + 8 * r) * a.c.heads + h) * D;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          const uint4 w = r ? w1[j] : w0[j];
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = (float)(int)(signed char)(x[2 * u + (i >> 2)] >> (8 * (i & 3))) * f;
+            *reinterpret_cast<uint4*>(to + 64 * j + 16 * c + 8 * u) = pack8<T>(v);
+          }
+        }
+      }
     }
-    if (at >= 0) *reinterpret_cast<uint4*>(out + ((size_t)(t0 + row) * a.c.heads + head) * D + 8 * l) = o;
   }
 }
 
@@ -292,24 +553,25 @@ int launch_cache_write(const CacheCall& c) {
   a.B = c.B, a.T = c.T, a.width = c.width;
   const int P = c.cache->page, D = c.cache->d;
   // pages touched: at least one token each, and at most two partly filled for each sequence
-  const long long units = std::min<long long>(c.T, (long long)c.T / P + 2ll * c.B);
-  const dim3 grid((unsigned)units, (unsigned)c.cache->heads, 2u);
-  const int passes = (P * (D / 8) + kThreads - 1) / kThreads;
+  a.units = (int)std::min<long long>(c.T, (long long)c.T / P + 2ll * c.B);
+  const int wpu = P / 16, per_cta = wpu < 4 ? 4 / wpu : 1;
+  const dim3 grid((unsigned)((a.units + per_cta - 1) / per_cta), (unsigned)c.cache->heads, 2u);
+  const int threads = wpu < 4 ? 128 : 32 * wpu;
   cudaStream_t s = (cudaStream_t)c.stream;
-  auto go = [&](auto kern) { kern<<<grid, kThreads, 0, s>>>(a); };
-#define OQ_PASSES(T, DD)                               \
-  switch (passes) {                                    \
-    case 1: go(write_kernel<T, DD, 1>); break;         \
-    case 2: go(write_kernel<T, DD, 2>); break;         \
-    case 4: go(write_kernel<T, DD, 4>); break;         \
-    default: go(write_kernel<T, DD, DD / 16>); break;  \
+  auto go = [&](auto kern) { kern<<<grid, threads, 0, s>>>(a); };
+#define OQ_WARPS(T, DD)                            \
+  switch (wpu) {                                   \
+    case 1: go(write_kernel<T, DD, 1>); break;     \
+    case 2: go(write_kernel<T, DD, 2>); break;     \
+    case 4: go(write_kernel<T, DD, 4>); break;     \
+    default: go(write_kernel<T, DD, 8>); break;    \
   }
   if (c.dtype == OQ_BF16) {
-    if (D == 128) OQ_PASSES(__nv_bfloat16, 128) else OQ_PASSES(__nv_bfloat16, 64)
+    if (D == 128) OQ_WARPS(__nv_bfloat16, 128) else OQ_WARPS(__nv_bfloat16, 64)
   } else {
-    if (D == 128) OQ_PASSES(__half, 128) else OQ_PASSES(__half, 64)
+    if (D == 128) OQ_WARPS(__half, 128) else OQ_WARPS(__half, 64)
   }
-#undef OQ_PASSES
+#undef OQ_WARPS
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "cache write launch: %s", cudaGetErrorString(e));
   return OQ_OK;
@@ -327,13 +589,13 @@ int launch_cache_read(const CacheCall& c) {
   const int D = c.cache->d;
   int nsm;
   if (int rc = sm_count(&nsm)) return rc;
-  // enough rows for a CTA to keep its loads in flight, fewer while SMs stand idle
-  const int pass = kThreads / (D / 8);
-  int rows = 128;
-  while (rows > pass && (long long)((c.T + rows - 1) / rows) * c.cache->heads * 2 < 4ll * nsm) rows /= 2;
-  const dim3 grid((unsigned)((c.T + rows - 1) / rows), (unsigned)c.cache->heads, 2u);
+  // a warp finds its rows' places once for several heads, as far as there are warps for all SMs
+  const long long tiles = (c.T + 15) / 16;
+  a.heads_warp = (int)std::max<long long>(1, std::min<long long>(8, 2 * tiles * c.cache->heads / (32ll * nsm)));
+  const dim3 grid((unsigned)((tiles + kThreads / 32 - 1) / (kThreads / 32)),
+                  (unsigned)((c.cache->heads + a.heads_warp - 1) / a.heads_warp), 2u);
   cudaStream_t s = (cudaStream_t)c.stream;
-  auto go = [&](auto kern) { kern<<<grid, kThreads, 0, s>>>(a, rows); };
+  auto go = [&](auto kern) { kern<<<grid, kThreads, 0, s>>>(a); };
   if (c.dtype == OQ_BF16)
     D == 128 ? go(read_kernel<__nv_bfloat16, 128>) : go(read_kernel<__nv_bfloat16, 64>);
   else

@@ -372,27 +372,27 @@ class KVCache:
                 raise ValueError("cache tensors must be contiguous and on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.heads, self.page, self.d = k.shape
-        self.device = k.device
+        self.device, self._index = k.device, k.get_device()
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                     self.n_pages, self.heads, self.page, self.d)
         self._ref = ctypes.byref(self._struct)
 
 
-# The calls below cost a few microseconds on the host, which is what small launches
-# are paced by: checks look at each tensor once, and the current device and
-# stream come from the raw getters that torch.cuda's own objects are made from.
+# The calls below are paced by the host where the work is small, so each looks at its
+# tensors in as few steps as Python has: devices as their numbers, one expression for
+# the checks, and the words of an error only when one fails.
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
+_I32 = torch.int32
 
 
-def _launch(fn, device, stream, *args):
-    """fn(*args, stream) with the tensors' device current."""
-    index = device.index
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device (got {device})")
+def _launch(fn, index, stream, *args):
+    """fn(*args, stream) with the tensors' device (its number) current."""
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
     if index != _current_device():
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
         rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
@@ -400,38 +400,33 @@ def _launch(fn, device, stream, *args):
         _check(rc)
 
 
-def _rows(name, t, heads, d):
-    """Strides (token, head) of [T, heads, d] rows and the dtype's code; checks
-    what the library cannot see (heads, d: None for any)."""
-    shape, strides, dtype = t.shape, t.stride(), DTYPES.get(t.dtype)
-    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (d is not None and shape[2] != d):
-        raise ValueError(f"{name} must be [T, {heads or 'heads'}, {d or 'd'}] (got {tuple(shape)})")
-    if strides[2] != 1 and shape[2] > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if dtype is None:
-        raise ValueError(f"{name}: dtype {t.dtype} is not supported")
-    return strides[0], strides[1], dtype
+def _rows(name, t, index, heads, d, T=None, dtype=None):
+    """Strides (token, head) of rows [T, heads, d] on device `index` (heads, d, T,
+    dtype: None for any)."""
+    shape, strides = t.shape, t.stride()
+    if (len(shape) == 3 and strides[2] == 1 and t.get_device() == index and (d is None or shape[2] == d)
+            and (heads is None or shape[1] == heads) and (T is None or shape[0] == T)
+            and (t.dtype in DTYPES if dtype is None else t.dtype is dtype)):
+        return strides
+    if len(shape) == 3 and shape[2] == 1 and strides[2] != 1:  # one element: any stride
+        return _rows(name, t.as_strided(shape, (strides[0], strides[1], 1)), index, heads, d, T, dtype)
+    raise ValueError(f"{name} must be [{'T' if T is None else T}, {heads or 'heads'}, {d or 'd'}] rows of "
+                     f"{dtype or 'bf16, fp16 or fp32'}, each contiguous, on device {index} "
+                     f"(got {t.dtype} {list(shape)}, strides {list(strides)}, on {t.device})")
 
 
-def _alike(name, t, like):
-    if t.shape[0] != like.shape[0] or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must match in tokens, dtype and device (got {tuple(t.shape)}, {t.dtype}, {t.device})")
-
-
-def _index(name, t, device, shape):
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {device} "
-                         f"(got {t.dtype} {list(t.shape)} on {t.device})")
-    return t.data_ptr()
-
-
-def _batch(device, cu, at_name, at, table):
+def _batch(cache, cu, at_name, at, table):
     """Pointers of a batch's index tensors, and B and the table's width."""
-    if at.dim() != 1 or table.dim() != 2:
-        raise ValueError(f"{at_name} must be [B] and table [B, width] (got {tuple(at.shape)}, {tuple(table.shape)})")
-    B, width = at.shape[0], table.shape[1]
-    return (_index("cu", cu, device, (B + 1,)), _index(at_name, at, device, (B,)), B,
-            _index("table", table, device, (B, width)), width)
+    index, B, width = cache._index, at.shape, table.shape
+    if (len(B) == 1 and len(width) == 2 and width[0] == B[0] and cu.shape == (B[0] + 1,)
+            and cu.dtype is _I32 and at.dtype is _I32 and table.dtype is _I32
+            and cu.get_device() == index and at.get_device() == index and table.get_device() == index
+            and cu.is_contiguous() and at.is_contiguous() and table.is_contiguous()):
+        return cu.data_ptr(), at.data_ptr(), B[0], table.data_ptr(), width[1]
+    said = ", ".join(f"{n} {t.dtype} {list(t.shape)} on {t.device}"
+                     for n, t in (("cu", cu), (at_name, at), ("table", table)))
+    raise ValueError(f"cu [B + 1], {at_name} [B] and table [B, width] must be contiguous int32 on {cache.device} "
+                     f"(got {said})")
 
 
 def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out=None, inverse: bool = False, stream=None):
@@ -439,17 +434,18 @@ def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out=None, inverse
     tokens and heads) turned by pos: int32 [T, axes].  out: written and returned
     (x itself: in place); a new tensor if None.  inverse: the transposed turn,
     which is also the gradient."""
-    xt, xh, code = _rows("x", x, None, None)
+    index = x.get_device()
+    sx = _rows("x", x, index, None, None)
     T, heads, d = x.shape
+    dtype = x.dtype
     if out is None:
-        out = torch.empty((T, heads, d), dtype=x.dtype, device=x.device)
-        ot, oh = heads * d, d
-    else:
-        ot, oh, _ = _rows("out", out, heads, d)
-        _alike("out", out, x)
-    device = x.device
-    _launch(_lib.oq_rope_apply, device, stream, rope._h, x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, code, T, heads, d,
-            _index("pos", pos, device, (T, rope.n_axes)), inverse)
+        out = torch.empty((T, heads, d), dtype=dtype, device=x.device)
+    so = _rows("out", out, index, heads, d, T, dtype)
+    if pos.dtype is not _I32 or pos.shape != (T, rope.n_axes) or pos.get_device() != index or not pos.is_contiguous():
+        raise ValueError(f"pos must be contiguous int32 [{T}, {rope.n_axes}] on x's device "
+                         f"(got {pos.dtype} {list(pos.shape)} on {pos.device})")
+    _launch(_lib.oq_rope_apply, index, stream, rope._h, x.data_ptr(), sx[0], sx[1], out.data_ptr(), so[0], so[1],
+            DTYPES[dtype], T, heads, d, pos.data_ptr(), inverse)
     return out
 
 
@@ -458,15 +454,12 @@ def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tens
     """Quantizes the rows k, v (cuda bf16 / fp16 [T, heads, d], rows cu[b] ..
     cu[b+1]-1 are sequence b's) into the cache behind the past[b] tokens that
     the sequence holds, in the pages of table: int32 [B, width]."""
-    kt, kh, code = _rows("k", k, cache.heads, cache.d)
-    vt, vh, _ = _rows("v", v, cache.heads, cache.d)
-    _alike("v", v, k)
-    device = cache.device
-    if k.device != device:
-        raise ValueError(f"k and v must be on the cache's device {device}")
-    cu_p, at_p, B, table_p, width = _batch(device, cu, "past", past, table)
-    _launch(_lib.oq_cache_write, device, stream, cache._ref, None if rpbh is None else rpbh._h, k.data_ptr(), kt, kh,
-            v.data_ptr(), vt, vh, code, k.shape[0], cu_p, at_p, B, table_p, width)
+    index, T, dtype = cache._index, k.shape[0], k.dtype
+    sk = _rows("k", k, index, cache.heads, cache.d)
+    sv = _rows("v", v, index, cache.heads, cache.d, T, dtype)
+    cu_p, at_p, B, table_p, width = _batch(cache, cu, "past", past, table)
+    _launch(_lib.oq_cache_write, index, stream, cache._ref, None if rpbh is None else rpbh._h, k.data_ptr(), sk[0], sk[1],
+            v.data_ptr(), sv[0], sv[1], DTYPES[dtype], T, cu_p, at_p, B, table_p, width)
 
 
 def cache_read(cache: KVCache, cu: torch.Tensor, first: torch.Tensor, table: torch.Tensor, T: int = None,
@@ -474,19 +467,18 @@ def cache_read(cache: KVCache, cu: torch.Tensor, first: torch.Tensor, table: tor
     """Reads tokens first[b] .. of every sequence b back into rows cu[b] ..
     cu[b+1]-1 of k and v ([T, heads, d] contiguous; made as `dtype` if not
     passed, with T rows)."""
-    if (k is None) != (v is None) or (k is None and T is None):
-        raise ValueError("pass k and v, or T")
-    device = cache.device
-    if k is None:
-        k, v = (torch.empty((T, cache.heads, cache.d), dtype=dtype, device=device) for _ in range(2))
-    _, _, code = _rows("k", k, cache.heads, cache.d)
-    _rows("v", v, cache.heads, cache.d)
-    _alike("v", v, k)
-    if not k.is_contiguous() or not v.is_contiguous() or k.device != device or (T is not None and T != k.shape[0]):
-        raise ValueError("k and v must be contiguous, of T rows, on the cache's device")
-    cu_p, at_p, B, table_p, width = _batch(device, cu, "first", first, table)
-    _launch(_lib.oq_cache_read, device, stream, cache._ref, None if rpbh is None else rpbh._h, k.data_ptr(),
-            v.data_ptr(), code, k.shape[0], cu_p, at_p, B, table_p, width)
+    if k is None or v is None:
+        if k is not None or v is not None or T is None:
+            raise ValueError("pass k and v, or T")
+        k, v = (torch.empty((T, cache.heads, cache.d), dtype=dtype, device=cache.device) for _ in range(2))
+    index, dtype = cache._index, k.dtype
+    _rows("k", k, index, cache.heads, cache.d, T)
+    _rows("v", v, index, cache.heads, cache.d, k.shape[0], dtype)
+    if not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("k and v must be contiguous")
+    cu_p, at_p, B, table_p, width = _batch(cache, cu, "first", first, table)
+    _launch(_lib.oq_cache_read, index, stream, cache._ref, None if rpbh is None else rpbh._h, k.data_ptr(), v.data_ptr(),
+            DTYPES[dtype], k.shape[0], cu_p, at_p, B, table_p, width)
     return k, v
 
 
@@ -500,24 +492,19 @@ def cache_attention(cache: KVCache, q: torch.Tensor, cu: torch.Tensor, lens: tor
     """Attention of the rows q (cuda bf16 / fp16 [T, heads, d], rows cu[b] ..
     cu[b+1]-1 are sequence b's newest tokens) over the lens[b] tokens that the
     sequence holds in the cache, these among them.  scale: 1/sqrt(d) if None."""
-    qt, qh, code = _rows("q", q, None, cache.d)
+    index, dtype = cache._index, q.dtype
+    sq = _rows("q", q, index, None, cache.d)
     T, heads, d = q.shape
-    device = cache.device
-    if q.device != device:
-        raise ValueError(f"q must be on the cache's device {device}")
     if out is None:
-        out = torch.empty((T, heads, d), dtype=q.dtype, device=device)
-        ot, oh = heads * d, d
-    else:
-        ot, oh, _ = _rows("out", out, heads, d)
-        _alike("out", out, q)
-    cu_p, at_p, B, table_p, width = _batch(device, cu, "lens", lens, table)
+        out = torch.empty((T, heads, d), dtype=dtype, device=cache.device)
+    so = _rows("out", out, index, heads, d, T, dtype)
+    cu_p, at_p, B, table_p, width = _batch(cache, cu, "lens", lens, table)
     if workspace is None:
         need = _lib.oq_cache_attention_workspace_bytes(cache._ref, T, B, heads)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
+        workspace = torch.empty((need,), dtype=torch.uint8, device=cache.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on q's device")
-    _launch(_lib.oq_cache_attention, device, stream, cache._ref, None if rpbh is None else rpbh._h, q.data_ptr(), qt, qh,
-            out.data_ptr(), ot, oh, code, heads, T, cu_p, at_p, B, table_p, width, causal,
+    _launch(_lib.oq_cache_attention, index, stream, cache._ref, None if rpbh is None else rpbh._h, q.data_ptr(), sq[0],
+            sq[1], out.data_ptr(), so[0], so[1], DTYPES[dtype], heads, T, cu_p, at_p, B, table_p, width, causal,
             d ** -0.5 if scale is None else scale, workspace.data_ptr(), workspace.nbytes)
     return out

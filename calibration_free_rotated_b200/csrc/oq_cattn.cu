@@ -25,7 +25,7 @@
 // 64 rows at least and its operands expanded into shared memory; eight rows
 // would leave it idle, and the kernel waits for memory, not for products.)
 //
-// A warp keeps a ring of four 16-token stages of its own, filled by 16-byte
+// A warp keeps a ring of 16-token stages of its own, filled by 16-byte
 // asynchronous copies, so it never waits for other warps while tiles run; the
 // four warps of a CTA take turns over the tokens and put their sums together at
 // the end of an item.
@@ -41,7 +41,6 @@ namespace {
 using namespace cattn;
 
 constexpr int kThreads = 128, kWarps = 4;
-constexpr int kStages = 4;
 constexpr int kTile = 64;  // keys of a tile: 16 for each warp
 constexpr int kStart = 2;  // units of an item's beginning and end
 
@@ -83,13 +82,14 @@ __device__ __forceinline__ int value_at(int row, int chunk) {
 template <int D, int NQ, bool TWO>
 struct Smem {
   static constexpr int RT = 8 * NQ;
+  static constexpr int kStages = NQ == 1 ? 3 : 4;  // three: four CTAs an SM
   static constexpr int kStageBytes = 2 * 16 * D;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kScales = kRing;                             // [warps][stages][2] floats
   static constexpr int kQ = kScales + kWarps * kStages * 8;         // [RT][D + 8] halves
   static constexpr int kLow = kQ + RT * (D + 8) * 2;                // the same: the query's second term
-  static constexpr int kRow = kLow + (TWO ? RT * (D + 8) * 2 : 0);  // [RT] factor, [RT] limit
-  static constexpr int kStat = kRow + RT * 8;                       // [warps][RT] maximum, sum
+  static constexpr int kRow = kLow + (TWO ? RT * (D + 8) * 2 : 0);  // [RT] factor, [RT] limit, [RT] start of the scores
+  static constexpr int kStat = kRow + RT * 12;                      // [warps][RT] maximum, sum
   static constexpr int kStageRow = kStat + kWarps * RT * 8;         // [128 / (D / 8)][D] 16-bit rows
   static constexpr int kTotal = kStageRow + kThreads / (D / 8) * D * 2;
   static constexpr int kSumStride = D + 4;
@@ -98,10 +98,10 @@ struct Smem {
 };
 
 template <typename T, int D, int NQ, bool TWO>
-__global__ void __launch_bounds__(kThreads, NQ == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 2)
 step_kernel(const __grid_constant__ Args a) {
   using S = Smem<D, NQ, TWO>;
-  constexpr int RT = S::RT, LPR = D / 8, KS = D / 16;
+  constexpr int RT = S::RT, LPR = D / 8, KS = D / 16, kStages = S::kStages;
   extern __shared__ __align__(16) unsigned char sm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -110,6 +110,7 @@ step_kernel(const __grid_constant__ Args a) {
   __half* low = reinterpret_cast<__half*>(sm + S::kLow);
   float* row_fac = reinterpret_cast<float*>(sm + S::kRow);
   int* row_lim = reinterpret_cast<int*>(sm + S::kRow + RT * 4);
+  float* row_bias = reinterpret_cast<float*>(sm + S::kRow + RT * 8);
   float* w_max = reinterpret_cast<float*>(sm + S::kStat);
   float* w_sum = w_max + kWarps * RT;
   float* sums = reinterpret_cast<float*>(sm);
@@ -127,6 +128,14 @@ step_kernel(const __grid_constant__ Args a) {
   const int l = lane % LPR;
   const LaneTurn turn = lane_turn(a.r, l);
   T* stage_row = reinterpret_cast<T*>(sm + S::kStageRow) + (threadIdx.x / LPR) * D;
+  const int plog = 31 - __clz(a.c.page);
+  // the lane's places in a stage: chunk lane + 32 j, of which j and j + 2 lie 1024 bytes apart
+  uint32_t to_key[2], to_value[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int id = lane + 32 * j;
+    to_key[j] = key_at<D>(id / KS, id % KS), to_value[j] = value_at<D>(id / KS, id % KS);
+  }
 
   while (at < stop && b < a.B) {
     const Seq s = load_seq(a, b, false);
@@ -173,20 +182,32 @@ step_kernel(const __grid_constant__ Args a) {
 #pragma unroll
       for (int m = LPR / 2; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
       const int e = min(max(scale_exp(top), -100), 120);
+      float all = 0.0f;  // of the row's terms: see the keys' products
       if (r < RT) {
         const float f = pow2(-e);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] *= f;
         const uint4 hi = pack8<__half>(x);
         *reinterpret_cast<uint4*>(qs + r * (D + 8) + 8 * l) = hi;
+        float y[8];
+        unpack8<__half>(hi, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) all += y[k];
         if constexpr (TWO) {
-          float y[8];
-          unpack8<__half>(hi, y);
 #pragma unroll
           for (int k = 0; k < 8; ++k) y[k] = x[k] - y[k];
-          *reinterpret_cast<uint4*>(low + r * (D + 8) + 8 * l) = pack8<__half>(y);
+          const uint4 lo = pack8<__half>(y);
+          *reinterpret_cast<uint4*>(low + r * (D + 8) + 8 * l) = lo;
+          unpack8<__half>(lo, y);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) all += y[k];
         }
+      }
+#pragma unroll
+      for (int m = LPR / 2; m >= 1; m >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, m);
+      if (r < RT) {
         if (l == 0) {
+          row_bias[r] = -1152.0f * all;
           row_fac[r] = pow2(e) * a.scale;
           row_lim[r] = r >= rows ? 0 : a.causal ? s.len - s.n + i + 1 : s.len;
         }
@@ -194,7 +215,7 @@ step_kernel(const __grid_constant__ Args a) {
     }
     __syncthreads();
     uint32_t qf[NQ][KS][2];
-    float fac[NQ][2];
+    float fac[NQ][2], bias[NQ][2];
     int lim[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -205,7 +226,10 @@ step_kernel(const __grid_constant__ Args a) {
         qf[n][k][0] = w.x, qf[n][k][1] = w.y;
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fac[n][j] = row_fac[8 * n + 2 * c + j], lim[n][j] = row_lim[8 * n + 2 * c + j];
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * n + 2 * c + j;
+        fac[n][j] = row_fac[r], lim[n][j] = row_lim[r], bias[n][j] = row_bias[r];
+      }
     }
     const int sure = row_lim[0];  // keys before this are seen by every row of the tile
 
@@ -223,48 +247,52 @@ step_kernel(const __grid_constant__ Args a) {
 
     const int tok0 = t0 * kTile + warp * 16;
     const int* table = a.table + (size_t)b * a.width;
-    auto issue = [&](int k) {
+    auto issue = [&](int k, int st) {  // tokens of step k into stage st
       const int tok = tok0 + k * kTile;
       if (k < take && tok < keys) {
-        const int slot = tok / a.c.page, off = tok - slot * a.c.page;
-        int page = table[slot];
+        int page = table[tok >> plog];
         const int have = (page >= 0 && page < a.c.n_pages) ? 16 : 0;  // else zeros: a key scale of 0
         if (!have) {
           if (lane == 0) bad_index(a.status);
           page = 0;
         }
         const size_t ph = (size_t)page * a.c.heads + h;
-        const int8_t* ks = a.c.k + (ph * a.c.page + off) * D;
-        const int8_t* vs = a.c.v + (ph * a.c.page + off) * D;
-        const uint32_t dst = ring + (k % kStages) * S::kStageBytes;
+        const size_t from = ((ph << plog) + (tok & (a.c.page - 1))) * D + 16 * lane;
+        const int8_t* ks = a.c.k + from;
+        const int8_t* vs = a.c.v + from;
+        const uint32_t dst = ring + st * S::kStageBytes;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const int id = lane + 32 * j, row = id / KS, ch = id % KS;
-          copy16(dst + key_at<D>(row, ch), ks + 16 * id, have);
-          copy16(dst + 16 * D + value_at<D>(row, ch), vs + 16 * id, have);
+          copy16(dst + to_key[j & 1] + (j >> 1) * 1024, ks + 512 * j, have);
+          copy16(dst + 16 * D + to_value[j & 1] + (j >> 1) * 1024, vs + 512 * j, have);
         }
-        if (lane < 2) copy4(scales_s + (k % kStages) * 8 + 4 * lane, (lane ? a.c.vs : a.c.ks) + ph, have / 4);
+        if (lane < 2) copy4(scales_s + st * 8 + 4 * lane, (lane ? a.c.vs : a.c.ks) + ph, have / 4);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) issue(k);
+    for (int k = 0; k < kStages - 1; ++k) issue(k, k);
+    int now = 0, then = kStages - 1;  // stages of step k, of the one that is fetched
 
     for (int k = 0; k < take; ++k) {
       const int tok = tok0 + k * kTile;
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();
-      issue(k + kStages - 1);
+      issue(k + kStages - 1, then);
       if (tok >= keys) break;  // the same for the warp; only the item's last tile ends early
-      const unsigned char* st = ring_p + (k % kStages) * S::kStageBytes;
-      const float kscale = scales_p[(k % kStages) * 2], vscale = scales_p[(k % kStages) * 2 + 1];
+      const unsigned char* st = ring_p + now * S::kStageBytes;
+      const float kscale = scales_p[now * 2], vscale = scales_p[now * 2 + 1];
+      now = now + 1 == kStages ? 0 : now + 1, then = then + 1 == kStages ? 0 : then + 1;
       const int ev = min(max(scale_exp(vscale), -126), 126);
 
+      // The keys' codes go into the products as 1152 + code (see oq_cattn.cuh) and the
+      // sums begin at -1152 times the query's: the difference is the product with the
+      // codes, to 2^-24 of ~2^13, far below what the query's rounding leaves.
       float sc[NQ][4];
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[n][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) sc[n][j] = bias[n][j & 1];
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
         const uint4 k0 = *reinterpret_cast<const uint4*>(st + key_at<D>(g, 4 * j + c));
@@ -273,8 +301,8 @@ step_kernel(const __grid_constant__ Args a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t x0 = w0[i] ^ 0x80808080u, x1 = w1[i] ^ 0x80808080u;
-          const uint32_t a0 = bytes2(x0, 0x4140), a1 = bytes2(x1, 0x4140), a2 = bytes2(x0, 0x4342),
-                         a3 = bytes2(x1, 0x4342);
+          const uint32_t a0 = __byte_perm(x0, 0x64646464u, 0x4140), a1 = __byte_perm(x1, 0x64646464u, 0x4140),
+                         a2 = __byte_perm(x0, 0x64646464u, 0x4342), a3 = __byte_perm(x1, 0x64646464u, 0x4342);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
             mma16816(sc[n], a0, a1, a2, a3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
@@ -286,21 +314,27 @@ step_kernel(const __grid_constant__ Args a) {
         }
       }
       // scores to base 2 plus the values' exponent; rows of sc: tokens g, g + 8; columns: rows 2 c, 2 c + 1
-      bool raise = false;
-      const bool whole = tok + 16 <= sure && kscale != 0.0f;
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float s0 = fmaf(sc[n][j], kscale * fac[n][j], (float)ev);
-          float s1 = fmaf(sc[n][2 + j], kscale * fac[n][j], (float)ev);
-          if (!whole) {
-            if (tok + g >= lim[n][j] || kscale == 0.0f) s0 = -INFINITY;
-            if (tok + g + 8 >= lim[n][j] || kscale == 0.0f) s1 = -INFINITY;
-          }
-          sc[n][j] = s0, sc[n][2 + j] = s1;
-          raise |= fmaxf(s0, s1) > top[n][j] + kRaise;
+          sc[n][j] = fmaf(sc[n][j], kscale * fac[n][j], (float)ev);
+          sc[n][2 + j] = fmaf(sc[n][2 + j], kscale * fac[n][j], (float)ev);
         }
+      if (tok + 16 > sure || kscale == 0.0f) {  // the same for the warp
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (tok + g >= lim[n][j] || kscale == 0.0f) sc[n][j] = -INFINITY;
+            if (tok + g + 8 >= lim[n][j] || kscale == 0.0f) sc[n][2 + j] = -INFINITY;
+          }
+      }
+      bool raise = false;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) raise |= fmaxf(sc[n][j], sc[n][2 + j]) > top[n][j] + kRaise;
       if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {

@@ -112,6 +112,27 @@ __device__ Share find_share(const Args& a, int cta, int ctas) {
   __shared__ long long warp_sum[THREADS / 32];
   __shared__ Share found;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (a.B <= 32) {  // each warp finds it for itself
+    long long mine = 0;
+    if (lane < a.B) {
+      const Seq s = load_seq(a, lane, cta == 0 && warp == 0);
+      mine = units_before<RT, TILE, START>(a, s, row_tiles<RT>(s)) * a.c.heads;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+      if (lane >= m) incl += o;
+    }
+    Share s;
+    s.total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    s.size = (s.total + ctas - 1) / ctas;
+    const long long start = s.size * cta;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, start >= incl - mine && start < incl);
+    s.b = hit ? __ffs(hit) - 1 : a.B;
+    s.into = start - __shfl_sync(0xFFFFFFFFu, incl - mine, hit ? s.b : 0);
+    return s;
+  }
   long long total = 0, mine = 0, start = 0, size = 0;
   if (threadIdx.x == 0) found.b = a.B;
   // two passes over the sequences: the sum, then the one that holds the start;

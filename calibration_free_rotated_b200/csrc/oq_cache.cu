@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(WPU < 4 ? 128 : 32 * WPU) write_kernel(const _
   constexpr int KS = D / 16, PITCH = D + 4;  // words of a row pair in shared memory
   __shared__ __align__(16) uint32_t stage[WARPS][8 * PITCH];
   __shared__ uint32_t warp_top[WARPS];
+  chain();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int unit = blockIdx.x * UNITS + warp / WPU, row0 = 16 * (warp % WPU);
   const int head = blockIdx.y;
@@ -384,6 +385,7 @@ template <typename T, int D, bool TURN>
 __global__ void __launch_bounds__(kThreads, 4) read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int KS = D / 16, PITCH = D + 4;
   __shared__ __align__(16) uint32_t stage[TURN ? kThreads / 32 : 1][8 * PITCH];
+  chain();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int plog = 31 - __clz(a.c.page);
   uint32_t m[2][2];
@@ -574,8 +576,8 @@ int launch_cache_write(const CacheCall& c) {
   const int wpu = P / 16, per_cta = wpu < 4 ? 4 / wpu : 1;
   const dim3 grid((unsigned)((a.units + per_cta - 1) / per_cta), (unsigned)c.cache->heads, 2u);
   const int threads = wpu < 4 ? 128 : 32 * wpu;
-  cudaStream_t s = (cudaStream_t)c.stream;
-  auto go = [&](auto kern) { kern<<<grid, threads, 0, s>>>(a); };
+  int rc = OQ_OK;
+  auto go = [&](auto kern) { rc = launch_chained("cache write", kern, grid, threads, 0, c.stream, a); };
 #define OQ_WRITE(T, DD, W) a.r.perm ? go(write_kernel<T, DD, W, true>) : go(write_kernel<T, DD, W, false>)
 #define OQ_WARPS(T, DD)                    \
   switch (wpu) {                           \
@@ -591,9 +593,7 @@ int launch_cache_write(const CacheCall& c) {
   }
 #undef OQ_WARPS
 #undef OQ_WRITE
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "cache write launch: %s", cudaGetErrorString(e));
-  return OQ_OK;
+  return rc;
 }
 
 int launch_cache_read(const CacheCall& c) {
@@ -616,8 +616,8 @@ int launch_cache_read(const CacheCall& c) {
   a.heads_warp = (int)std::max<long long>(1, std::min<long long>(a.r.perm ? 8 : 2, 2 * tiles * c.cache->heads / (32ll * nsm)));
   const dim3 grid((unsigned)((tiles + kThreads / 32 - 1) / (kThreads / 32)),
                   (unsigned)((c.cache->heads + a.heads_warp - 1) / a.heads_warp), 2u);
-  cudaStream_t s = (cudaStream_t)c.stream;
-  auto go = [&](auto kern) { kern<<<grid, kThreads, 0, s>>>(a); };
+  int rc = OQ_OK;
+  auto go = [&](auto kern) { rc = launch_chained("cache read", kern, grid, kThreads, 0, c.stream, a); };
 #define OQ_READ(T, DD) a.r.perm ? go(read_kernel<T, DD, true>) : go(read_kernel<T, DD, false>)
   if (c.dtype == OQ_BF16) {
     if (D == 128) OQ_READ(__nv_bfloat16, 128);
@@ -627,9 +627,7 @@ int launch_cache_read(const CacheCall& c) {
     else OQ_READ(__half, 64);
   }
 #undef OQ_READ
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "cache read launch: %s", cudaGetErrorString(e));
-  return OQ_OK;
+  return rc;
 }
 
 }  // namespace oq

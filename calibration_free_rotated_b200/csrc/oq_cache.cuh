@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "oq_internal.h"
 
@@ -21,6 +22,34 @@ namespace cache {
 // 2^-40 are not resolved.  The bounds keep 2^(e_max - e_min) and its products
 // with exponentials of either sign inside fp32.
 constexpr int kExpMin = -40, kExpMax = 40;
+
+// Programmatic dependent launch: a kernel may start while the one before it in the
+// stream finishes.  Every thread of these kernels first waits for that one's end
+// (so the one after may rely on both), then lets the next one start: at once where
+// the kernel is short, at its end where the next one's waiting blocks would take
+// room beside a long one.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void chain() {
+  chain_wait();
+  chain_next();
+}
+template <typename Kernel, typename... A>
+int launch_chained(const char* what, Kernel kern, dim3 grid, int threads, size_t smem, void* stream, const A&... args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e == cudaSuccess ? OQ_OK : fail(OQ_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+}
 
 struct Rotation {
   const uint16_t* perm;   // pi, or nullptr for no rotation

@@ -56,7 +56,7 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) 
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -64,7 +64,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -103,6 +103,7 @@ step_kernel(const __grid_constant__ Args a) {
   using S = Smem<D, NQ, TWO>;
   constexpr int RT = S::RT, LPR = D / 8, KS = D / 16, kStages = S::kStages;
   extern __shared__ __align__(16) unsigned char sm[];
+  chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int cta = blockIdx.x;
@@ -288,11 +289,11 @@ step_kernel(const __grid_constant__ Args a) {
       // The keys' codes go into the products as 1152 + code (see oq_cattn.cuh) and the
       // sums begin at -1152 times the query's: the difference is the product with the
       // codes, to 2^-24 of ~2^13, far below what the query's rounding leaves.
-      float sc[NQ][4];
+      float sc[NQ][4], sd[NQ][4];  // two chains of products
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[n][j] = bias[n][j & 1];
+        for (int j = 0; j < 4; ++j) sc[n][j] = bias[n][j & 1], sd[n][j] = 0.0f;
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
         const uint4 k0 = *reinterpret_cast<const uint4*>(st + key_at<D>(g, 4 * j + c));
@@ -305,10 +306,10 @@ step_kernel(const __grid_constant__ Args a) {
                          a2 = __byte_perm(x0, 0x64646464u, 0x4342), a3 = __byte_perm(x1, 0x64646464u, 0x4342);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
-            mma16816(sc[n], a0, a1, a2, a3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
+            mma16816(i & 1 ? sd[n] : sc[n], a0, a1, a2, a3, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
             if constexpr (TWO) {
               const uint2 w = *reinterpret_cast<const uint2*>(low + (8 * n + g) * (D + 8) + 64 * j + 16 * c + 4 * i);
-              mma16816(sc[n], a0, a1, a2, a3, w.x, w.y);
+              mma16816(i & 1 ? sd[n] : sc[n], a0, a1, a2, a3, w.x, w.y);
             }
           }
         }
@@ -318,8 +319,8 @@ step_kernel(const __grid_constant__ Args a) {
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          sc[n][j] = fmaf(sc[n][j], kscale * fac[n][j], (float)ev);
-          sc[n][2 + j] = fmaf(sc[n][2 + j], kscale * fac[n][j], (float)ev);
+          sc[n][j] = fmaf(sc[n][j] + sd[n][j], kscale * fac[n][j], (float)ev);
+          sc[n][2 + j] = fmaf(sc[n][2 + j] + sd[n][2 + j], kscale * fac[n][j], (float)ev);
         }
       if (tok + 16 > sure || kscale == 0.0f) {  // the same for the warp
 #pragma unroll
@@ -459,6 +460,7 @@ step_kernel(const __grid_constant__ Args a) {
     if (first && !last) desc = make_int4((int)((item_end - 1) / sh.size) - cta + 1, b, h, qt);
     __syncthreads();
   }
+  chain_next();
   if (threadIdx.x == 0) a.desc[cta] = desc;
 }
 
@@ -478,7 +480,7 @@ size_t piece_bytes(const Plan& p, int d) { return sizeof(float) * 2 * (size_t)p.
 size_t stat_bytes(const Plan& p) { return sizeof(float) * 4 * (size_t)p.ctas * p.rows; }
 
 template <typename T, int D, int NQ, bool TWO>
-int launch_step(const Args& a, int ctas_most, cudaStream_t s) {
+int launch_step(const Args& a, int ctas_most, void* stream) {
   auto kern = step_kernel<T, D, NQ, TWO>;
   const int smem = Smem<D, NQ, TWO>::kTotal;
   int per_sm = 0, nsm = 0;
@@ -490,13 +492,8 @@ int launch_step(const Args& a, int ctas_most, cudaStream_t s) {
   const long long items = std::min<long long>((rows + 8 * NQ - 1) / (8 * NQ) + a.B, rows) * a.c.heads;
   const long long tiles = items * std::max<long long>(1, ((long long)a.width * a.c.page + kTile - 1) / kTile);
   const int ctas = (int)std::min<long long>(tiles, std::min(nsm * per_sm, ctas_most));
-  kern<<<ctas, kThreads, smem, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-  join_kernel<T, D, 8 * NQ, 4><<<dim3((unsigned)ctas, 8 * NQ), 128, 0, s>>>(a, 0);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention join launch: %s", cudaGetErrorString(e));
-  return OQ_OK;
+  if (int rc = launch_chained("attention", kern, dim3((unsigned)ctas), kThreads, smem, stream, a)) return rc;
+  return launch_chained("attention join", join_kernel<T, D, 8 * NQ, 8>, dim3((unsigned)ctas, 8 * NQ), 256, 0, stream, a);
 }
 
 }  // namespace
@@ -527,9 +524,8 @@ int launch_cattn(const AttnCall& c) {
   a.stat = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d));
   a.desc = reinterpret_cast<int4*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d) + stat_bytes(p));
   if (p.rows == 256) return launch_cattn_chunk(a, c.dtype, v->d, c.stream);
-  cudaStream_t s = (cudaStream_t)c.stream;
 #define OQ_STEP(T, D, TWO) \
-  return p.rows == 8 ? launch_step<T, D, 1, TWO>(a, p.ctas, s) : launch_step<T, D, 2, TWO>(a, p.ctas, s)
+  return p.rows == 8 ? launch_step<T, D, 1, TWO>(a, p.ctas, c.stream) : launch_step<T, D, 2, TWO>(a, p.ctas, c.stream)
   if (c.dtype == OQ_BF16) {
     if (v->d == 128) OQ_STEP(__nv_bfloat16, 128, false);
     OQ_STEP(__nv_bfloat16, 64, false);

@@ -222,65 +222,96 @@ __device__ __forceinline__ Part find_part(const Args& a, const Seq& s, long long
 }
 
 // Puts the pieces of cut items together and writes their rows.  Block (i, j): rows
-// of the item that CTA i began, 4 / WPR of them at a time, each by WPR warps that
-// take turns over the pieces (WPR = 4 where an item may have many pieces, 1 where
-// it has many rows).
+// of the item that CTA i began.  WPR = 8: one row at a time, whose pieces eight warps
+// share (an item may have many); WPR = 1: a row for each of four warps (an item has
+// many rows and few pieces).  The pieces' weights come first, all at once, so that
+// the loads of the pieces wait for nothing.
 template <typename T, int D, int RT, int WPR>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a, int pdl) {
-  constexpr int ROWS = 4 / WPR;
-  __shared__ __align__(16) float part[4][D];
-  __shared__ float part_sum[4];
-  __shared__ __align__(16) T row_out[4][D];
-  if (pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(WPR == 8 ? 256 : 128) join_kernel(const __grid_constant__ Args a) {
+  constexpr int WARPS = WPR == 8 ? 8 : 4, ROWS = WARPS / WPR, MOST = WPR == 8 ? kStepCtas : kChunkCtas;
+  __shared__ __align__(16) float part[WARPS][D];
+  __shared__ float2 weight[ROWS][MOST];  // of a piece: its factor, and that times its sum
+  __shared__ float warp_max[WARPS];
+  __shared__ __align__(16) T row_out[ROWS][D];
+  chain();
   const int4 d = a.desc[blockIdx.x];
   if (d.x <= 0) return;
   const Seq s = load_seq(a, d.y, false);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % WPR, row = warp / WPR;
   const int rows = min(RT, s.rows - d.w * RT);
   constexpr int V = D / 32;  // values of a lane
-  for (int r0 = blockIdx.y * ROWS; r0 < rows; r0 += gridDim.y * ROWS) {
-    const int r = min(r0 + warp / WPR, rows - 1);
-    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * RT + r; };
-    float top = -INFINITY;
-    for (int i = lane; i < d.x; i += 32) top = fmaxf(top, a.stat[2 * slot(i)]);
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-    if (top == -INFINITY) top = 0.0f;
-    float o[V], sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = 0.0f;
-#pragma unroll 4
-    for (int i = warp % WPR; i < d.x; i += WPR) {
-      const size_t at = slot(i);
-      const float2 st = *reinterpret_cast<const float2*>(a.stat + 2 * at);
-      const float f = exp2f(st.x - top);
-      if (f == 0.0f) continue;  // nothing there: its values may not even be written
-      sum = fmaf(f, st.y, sum);
-      const float* p = a.piece + at * D + V * lane;
-      if constexpr (V == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]), o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(p);
-        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) part[warp][V * lane + k] = o[k];
-    if (lane == 0) part_sum[warp] = sum;
+  auto sync = [&] {
     if constexpr (WPR == 1)
       __syncwarp();
     else
       __syncthreads();
-    if (warp % WPR == 0) {
+  };
+  for (int r0 = blockIdx.y * ROWS; r0 < rows; r0 += gridDim.y * ROWS) {
+    const int r = min(r0 + row, rows - 1);
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * RT + r; };
+    float top = -INFINITY;
+    for (int i = 32 * w0 + lane; i < d.x; i += 32 * WPR) {
+      weight[row][i] = *reinterpret_cast<const float2*>(a.stat + 2 * slot(i));
+      top = fmaxf(top, weight[row][i].x);
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+    if constexpr (WPR > 1) {
+      if (lane == 0) warp_max[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) top = fmaxf(top, warp_max[w]);
+    }
+    if (top == -INFINITY) top = 0.0f;
+    for (int i = 32 * w0 + lane; i < d.x; i += 32 * WPR) {
+      const float2 st = weight[row][i];
+      const float f = exp2f(st.x - top);
+      weight[row][i] = make_float2(f, f == 0.0f ? 0.0f : f * st.y);
+    }
+    sync();
+    float o[V], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = 0.0f;
+    for (int i0 = w0; i0 < d.x; i0 += 8 * WPR) {
+      float v[8][V];
+      float2 f[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = min(i0 + u * WPR, d.x - 1);
+        f[u] = i0 + u * WPR < d.x ? weight[row][i] : make_float2(0.0f, 0.0f);
+        const float* p = a.piece + slot(i) * D + V * lane;
+        if constexpr (V == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(p);
+          v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(p);
+          v[u][0] = x.x, v[u][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        sum += f[u].y;
+#pragma unroll
+        for (int k = 0; k < V; ++k)  // (a piece of no weight: its values may not even be written)
+          o[k] = fmaf(f[u].x, f[u].x == 0.0f ? 0.0f : v[u][k], o[k]);
+      }
+    }
+    // each piece's sum was counted by the one warp that took it
+#pragma unroll
+    for (int k = 0; k < V; ++k) part[warp][V * lane + k] = o[k];
+    if constexpr (WPR > 1) {
+      __syncthreads();
+      if (lane == 0) warp_max[warp] = sum;
+    }
+    sync();
+    if (w0 == 0) {
       const int l = lane % (D / 8);
       float x[8];
-      sum = part_sum[warp];
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = part[warp][8 * l + k];
 #pragma unroll
       for (int w = 1; w < WPR; ++w) {
-        sum += part_sum[warp + w];
+        sum += warp_max[warp + w];
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] += part[warp + w][8 * l + k];
       }
@@ -289,21 +320,18 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
       for (int k = 0; k < 8; ++k) x[k] *= inv;
       uint4 w;
       if (a.r.perm) {
-        unrotate_row<T>(x, lane_turn(a.r, l), l, a.r, row_out[warp]);  // lanes of one l write the same values
+        unrotate_row<T>(x, lane_turn(a.r, l), l, a.r, row_out[row]);  // lanes of one l write the same values
         __syncwarp();
-        w = *reinterpret_cast<const uint4*>(row_out[warp] + 8 * l);
+        w = *reinterpret_cast<const uint4*>(row_out[row] + 8 * l);
       } else {
         w = pack8<T>(x);
       }
       const int g = d.w * RT + r, i = row_token(a, g);
-      if (lane < D / 8 && r0 + warp / WPR < rows)
+      if (lane < D / 8 && r0 + row < rows)
         *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (long long)(s.cu0 + i) * a.ot +
                                   ((long long)d.z * a.group + (g - i * a.group)) * a.oh + 8 * l) = w;
     }
-    if constexpr (WPR == 1)
-      __syncwarp();
-    else
-      __syncthreads();
+    sync();
   }
 }
 

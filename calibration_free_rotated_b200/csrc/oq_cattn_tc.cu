@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   using S = Smem<D, TWO>;
   constexpr int KT = S::KT, HK = KT / 2, LPR = D / 8, VST = S::VST;
   extern __shared__ unsigned char sm_raw[];
+  chain_wait();
   unsigned char* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -933,6 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       tile_items[w] += tile_take[w] > 0;
     }
   }
+  chain_next();
   if (tid == 0) a.desc[cta] = desc;
   tc_fence_before();
   __syncthreads();
@@ -942,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 }
 
 template <typename T, int D, bool TWO>
-int launch(const Args& a, cudaStream_t s) {
+int launch(const Args& a, void* stream) {
   using S = Smem<D, TWO>;
   auto kern = chunk_kernel<T, D, TWO>;
   int per_sm = 0, nsm = 0;
@@ -954,23 +956,17 @@ int launch(const Args& a, cudaStream_t s) {
   const long long items = std::min<long long>((rows + kRows - 1) / kRows + a.B, rows) * a.c.heads;
   const long long units = items * (kStart + 1 + (long long)a.width * a.c.page / S::KT);
   const int ctas = (int)std::min<long long>(units, std::min(nsm, kChunkCtas));
-  kern<<<ctas, kThreads, S::kAlloc, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-  join_kernel<T, D, kRows, 1><<<dim3((unsigned)ctas, kRows / 4), 128, 0, s>>>(a, 0);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "attention join launch: %s", cudaGetErrorString(e));
-  return OQ_OK;
+  if (int rc = launch_chained("attention", kern, dim3((unsigned)ctas), kThreads, S::kAlloc, stream, a)) return rc;
+  return launch_chained("attention join", join_kernel<T, D, kRows, 1>, dim3((unsigned)ctas, kRows / 4), 128, 0, stream, a);
 }
 
 }  // namespace
 
 int launch_cattn_chunk(const cattn::Args& a, int dtype, int d, void* stream) {
-  cudaStream_t s = (cudaStream_t)stream;
-  if (dtype == OQ_BF16) return d == 128 ? launch<__nv_bfloat16, 128, false>(a, s) : launch<__nv_bfloat16, 64, false>(a, s);
+  if (dtype == OQ_BF16) return d == 128 ? launch<__nv_bfloat16, 128, false>(a, stream) : launch<__nv_bfloat16, 64, false>(a, stream);
   // fp16 rows that are not turned are exact in one term
-  if (!a.r.perm) return d == 128 ? launch<__half, 128, false>(a, s) : launch<__half, 64, false>(a, s);
-  return d == 128 ? launch<__half, 128, true>(a, s) : launch<__half, 64, true>(a, s);
+  if (!a.r.perm) return d == 128 ? launch<__half, 128, false>(a, stream) : launch<__half, 64, false>(a, stream);
+  return d == 128 ? launch<__half, 128, true>(a, stream) : launch<__half, 64, true>(a, stream);
 }
 
 }  // namespace oq

@@ -72,6 +72,7 @@ template <typename T, bool HALVES>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int vecs) {
   constexpr int N = Vec<T>::N;
   extern __shared__ float2 turns[];  // [tokens][pairs]
+  chain();
   const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.T - t0);
   const int h0 = blockIdx.y * a.head_share, nh = min(a.head_share, a.heads - h0);
   for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
@@ -176,17 +177,10 @@ int launch_rope(const RopeCall& c) {
   a.head_share = (c.heads + shares - 1) / shares;
   const dim3 grid((unsigned)blocks, (unsigned)((c.heads + a.head_share - 1) / a.head_share));
   const size_t smem = sizeof(float2) * (size_t)a.tokens * a.pairs;
-  cudaStream_t s = (cudaStream_t)c.stream;
-  auto go = [&](auto kern) { kern<<<grid, kThreads, smem, s>>>(a, vecs); };
-  if (c.dtype == OQ_BF16)
-    c.halves ? go(rope_kernel<__nv_bfloat16, true>) : go(rope_kernel<__nv_bfloat16, false>);
-  else if (c.dtype == OQ_FP16)
-    c.halves ? go(rope_kernel<__half, true>) : go(rope_kernel<__half, false>);
-  else
-    c.halves ? go(rope_kernel<float, true>) : go(rope_kernel<float, false>);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(OQ_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
-  return OQ_OK;
+  auto go = [&](auto kern) { return launch_chained("rope", kern, grid, kThreads, smem, c.stream, a, vecs); };
+  if (c.dtype == OQ_BF16) return c.halves ? go(rope_kernel<__nv_bfloat16, true>) : go(rope_kernel<__nv_bfloat16, false>);
+  if (c.dtype == OQ_FP16) return c.halves ? go(rope_kernel<__half, true>) : go(rope_kernel<__half, false>);
+  return c.halves ? go(rope_kernel<float, true>) : go(rope_kernel<float, false>);
 }
 
 }  // namespace oq

@@ -42,7 +42,7 @@ using namespace cattn;
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kTile = 64;  // keys of a tile: 16 for each warp
-constexpr int kStart = 2;  // units of an item's beginning and end
+constexpr int kStart = 4;  // units of an item's beginning and end
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -159,15 +159,50 @@ step_kernel(const __grid_constant__ Args a) {
     }
     const int rows = min(RT, s.rows - qt * RT);
 
-    // the item's query rows: turned, scaled by a power of two, fp16
+    // the item's query rows and the first codes are fetched together
+    constexpr int PASS = kThreads / LPR, PASSES = (RT + PASS - 1) / PASS;
+    uint4 q_row[PASSES];
 #pragma unroll
-    for (int p = 0; p < RT; p += kThreads / LPR) {
-      const int r = p + threadIdx.x / LPR;
-      const int gr = qt * RT + min(r, rows - 1), i = row_token(a, gr);
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = p * PASS + threadIdx.x / LPR, gr = qt * RT + min(r, rows - 1), i = row_token(a, gr);
+      q_row[p] = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows)
-        w = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + i) * a.qt +
-                                            ((long long)h * a.group + (gr - i * a.group)) * a.qh + 8 * l);
+        q_row[p] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (long long)(s.cu0 + i) * a.qt +
+                                                   ((long long)h * a.group + (gr - i * a.group)) * a.qh + 8 * l);
+    }
+    const int tok0 = t0 * kTile + warp * 16;
+    const int* table = a.table + (size_t)b * a.width;
+    auto issue = [&](int k, int st) {  // tokens of step k into stage st
+      const int tok = tok0 + k * kTile;
+      if (k < take && tok < keys) {
+        int page = table[tok >> plog];
+        const int have = (page >= 0 && page < a.c.n_pages) ? 16 : 0;  // else zeros: a key scale of 0
+        if (!have) {
+          if (lane == 0) bad_index(a.status);
+          page = 0;
+        }
+        const size_t ph = (size_t)page * a.c.heads + h;
+        const size_t from = ((ph << plog) + (tok & (a.c.page - 1))) * D + 16 * lane;
+        const int8_t* ks = a.c.k + from;
+        const int8_t* vs = a.c.v + from;
+        const uint32_t dst = ring + st * S::kStageBytes;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          copy16(dst + to_key[j & 1] + (j >> 1) * 1024, ks + 512 * j, have);
+          copy16(dst + 16 * D + to_value[j & 1] + (j >> 1) * 1024, vs + 512 * j, have);
+        }
+        if (lane < 2) copy4(scales_s + st * 8 + 4 * lane, (lane ? a.c.vs : a.c.ks) + ph, have / 4);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) issue(k, k);
+
+    // the rows: turned, scaled by a power of two, fp16
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = p * PASS + threadIdx.x / LPR, i = row_token(a, qt * RT + min(r, rows - 1));
+      const uint4 w = q_row[p];
       float x[8];
       if (a.r.perm) {
         *reinterpret_cast<uint4*>(stage_row + 8 * l) = w;
@@ -246,33 +281,6 @@ step_kernel(const __grid_constant__ Args a) {
       for (int j = 0; j < 2; ++j) top[n][j] = -INFINITY, sum[n][j] = 0.0f;
     }
 
-    const int tok0 = t0 * kTile + warp * 16;
-    const int* table = a.table + (size_t)b * a.width;
-    auto issue = [&](int k, int st) {  // tokens of step k into stage st
-      const int tok = tok0 + k * kTile;
-      if (k < take && tok < keys) {
-        int page = table[tok >> plog];
-        const int have = (page >= 0 && page < a.c.n_pages) ? 16 : 0;  // else zeros: a key scale of 0
-        if (!have) {
-          if (lane == 0) bad_index(a.status);
-          page = 0;
-        }
-        const size_t ph = (size_t)page * a.c.heads + h;
-        const size_t from = ((ph << plog) + (tok & (a.c.page - 1))) * D + 16 * lane;
-        const int8_t* ks = a.c.k + from;
-        const int8_t* vs = a.c.v + from;
-        const uint32_t dst = ring + st * S::kStageBytes;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          copy16(dst + to_key[j & 1] + (j >> 1) * 1024, ks + 512 * j, have);
-          copy16(dst + 16 * D + to_value[j & 1] + (j >> 1) * 1024, vs + 512 * j, have);
-        }
-        if (lane < 2) copy4(scales_s + st * 8 + 4 * lane, (lane ? a.c.vs : a.c.ks) + ph, have / 4);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) issue(k, k);
     int now = 0, then = kStages - 1;  // stages of step k, of the one that is fetched
 
     for (int k = 0; k < take; ++k) {

@@ -192,7 +192,7 @@ struct Part {
 template <int RT, int TILE, int START>
 __device__ __forceinline__ Part find_part(const Args& a, const Seq& s, long long per_head, long long into, long long left) {
   Part p;
-  p.h = (int)(into / per_head);
+  p.h = (into | per_head) >> 32 ? (int)(into / per_head) : (int)((unsigned)into / (unsigned)per_head);
   const long long rem = into - p.h * per_head;
   int lo = 0, hi = row_tiles<RT>(s);  // units_before(lo) <= rem < units_before(hi)
   long long before = 0, after = per_head;

@@ -479,7 +479,12 @@ struct Plan {
 Plan plan_of(int T, int B, int group) {
   Plan p;
   const long long per = ((long long)T * group + B - 1) / std::max(1, B);  // rows of a sequence, on average
-  p.rows = per <= 8 ? 8 : per <= 16 ? 16 : 256;
+  // 32 sequences of 3600 keys, 4 heads, fp16, D = 64, group 4; and one of 31200, 12 heads,
+  // bf16, D = 128 (us with tiles of 8, 16, 256 rows):
+  //   rows    4            8           16           24           32           48
+  //        28, 33, 81   31, 35, 81   46, 39, 81   62, 61, 82   78, 64, 82   105, 83, 83
+  //                     33, 31, 71   46, 34, 71   61, 51, 71   75, 51, 71   105, 69, 72
+  p.rows = per <= 8 ? 8 : per <= 48 ? 16 : 256;
   p.ctas = p.rows == 256 ? kChunkCtas : kStepCtas;
   return p;
 }

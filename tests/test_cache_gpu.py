@@ -16,6 +16,9 @@ Tolerances (eps = torch.finfo(dtype).eps, a rounding is off by eps / 2):
 """
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -516,6 +519,37 @@ def test_shared_pages_and_a_batch_beyond_one_block(oq):
     assert float((ko.double() - y.double()).norm() / y.double().norm()) < 0.03
 
 
+SPLITS = [  # new, past, heads, group, d, page, block, dtype, causal
+    # several short row tiles of a sequence
+    ([12, 30, 0, 5], [0, 700, 3, 64], 2, 2, 128, 64, 64, "fp16", True),
+    ([48], [2500], 2, 1, 64, 16, 64, "bf16", True),
+    ([3, 3], [1000, 0], 1, 16, 128, 32, 128, "bf16", True),
+    ([1, 1], [33, 800], 2, 40, 64, 64, 0, "bf16", True),
+    ([17, 40, 1], [90, 0, 2200], 1, 1, 128, 128, 128, "bf16", False),
+    # items cut between many CTAs, and many items for each of them
+    ([60], [9000], 1, 1, 128, 64, 128, "bf16", True),
+    ([70], [4100], 1, 1, 64, 16, 64, "fp16", False),
+    ([260, 1, 0, 520], [1000, 7, 0, 0], 3, 1, 128, 16, 128, "bf16", True),
+    ([257, 255, 256], [31, 64, 0], 8, 1, 64, 64, 64, "bf16", True),
+    ([30, 90] * 25, [40, 0] * 25, 3, 2, 64, 16, 64, "fp16", True),
+]
+
+
+@pytest.mark.parametrize("new,past,heads,group,d,page,block,dt,causal", SPLITS)
+def test_attention_work_split(oq, new, past, heads, group, d, page, block, dt, causal):
+    rng = np.random.default_rng(sum(new) + sum(past) + d)
+    r, rot = rotation(oq, d, block)
+    bt = Batch(rng, new, past, page)
+    cache = filled(oq, rng, bt, heads, d, r, dt)
+    q = rows(rng, (bt.T, heads * group, d), dt, loud=False) * 2
+    out = check_attention(oq, cache, bt, q, r, rot, causal)
+    # once more, into every other head and token of a larger tensor: the same bits, and nothing beside them
+    wide = torch.full((2 * bt.T, 2 * heads * group, d), 3.0, dtype=q.dtype, device="cuda")
+    oq.cache_attention(cache, q, ints(bt.cu), ints(bt.total), ints(bt.table), rpbh=r, causal=causal, out=wide[::2, 1::2])
+    assert torch.equal(wide[::2, 1::2][:bt.cu[-1]], out[:bt.cu[-1]])
+    assert torch.all(wide[1::2] == 3.0) and torch.all(wide[:, ::2] == 3.0)
+
+
 # ----------------------------------------------------------- streams, graphs, devices
 def test_streams_and_graphs(oq):
     """The operators on a stream of their own and in two captured graphs that share a workspace."""
@@ -568,6 +602,72 @@ def test_streams_and_graphs(oq):
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
     oq.device_status()
+
+
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_two_calls_at_once(oq, n):
+    """Two streams with a workspace each, over one cache, many calls in flight."""
+    rng = np.random.default_rng(34)
+    r, _ = rotation(oq, 64, 64)
+    bt = Batch(rng, [n, n], [700, 90], 16)
+    cache = filled(oq, rng, bt, 2, 64, r)
+    cu, total, table = ints(bt.cu), ints(bt.total), ints(bt.table)
+    q = [rows(rng, (bt.T, 4, 64), "bf16") for _ in range(2)]
+    want = [oq.cache_attention(cache, x, cu, total, table, rpbh=r) for x in q]
+    need = oq.cache_attention_workspace_bytes(cache, bt.T, 2, 4)
+    ws = [torch.empty((need,), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [[torch.zeros_like(q[0]) for _ in range(20)] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for j in range(2):
+            oq.cache_attention(cache, q[j], cu, total, table, rpbh=r, out=outs[j][i], workspace=ws[j], stream=streams[j])
+    torch.cuda.synchronize()
+    oq.device_status()
+    for j in range(2):
+        for o in outs[j]:
+            assert torch.equal(o, want[j])
+
+
+_CHILD = r"""
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+from calibration_free_rotated_b200 import orbitquant as oq
+torch.manual_seed(5)
+ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+r, rope, outs = oq.Rpbh(0, 128, 128), oq.Rope((16, 56, 56)), []
+x = torch.randn(90, 6, 128, device="cuda").bfloat16()
+pos = ints([[i, i // 7, i % 7] for i in range(90)])
+for rep in range(3):  # back to back: each launch follows one that it reads from or that used the workspace
+    cache = oq.KVCache(8, 2, 128, 32)
+    table = ints([[1, 2, 3, 6], [4, 0, 5, 7]])
+    for new, past in (([60, 30], [0, 0]), ([1, 1], [60, 30]), ([1, 2], [61, 31])):
+        T, cu = sum(new), ints([0, new[0], sum(new)])
+        kv = oq.rope_apply(rope, x[:T, :2], pos[:T])
+        q = oq.rope_apply(rope, x[:T, 2:], pos[:T])
+        oq.cache_write(cache, kv, x[:T, 1:3], cu, ints(past), table, rpbh=r)
+        outs.append(oq.cache_attention(cache, q, cu, ints([a + b for a, b in zip(new, past)]), table, rpbh=r))
+    outs += oq.cache_read(cache, ints([0, 62, 95]), ints([0, 0]), table, T=95, rpbh=r)
+    outs += [cache.k, cache.v, cache.k_scale, cache.v_scale]
+torch.cuda.synchronize()
+oq.device_status()
+n = len(outs) // 3
+assert all(torch.equal(a, b) for i in (1, 2) for a, b in zip(outs[:n], outs[i * n:]))
+torch.save([t.cpu() for t in outs[:n]], sys.argv[2])
+"""
+
+
+def test_the_same_with_and_without_programmatic_launches(oq, tmp_path):
+    """The chained launches change no result (OQ_NO_PDL is read once per process: child processes)."""
+    root, got = os.path.dirname(os.path.dirname(os.path.abspath(__file__))), []
+    for off in ("0", "1"):
+        path = str(tmp_path / off)
+        run = subprocess.run([sys.executable, "-c", _CHILD, root, path], env={**os.environ, "OQ_NO_PDL": off},
+                             capture_output=True, text=True, timeout=600)
+        assert run.returncode == 0, run.stderr[-2000:]
+        got.append(torch.load(path))
+    assert len(got[0]) == len(got[1]) and all(torch.equal(a, b) for a, b in zip(*got))
 
 
 def test_no_library_allocations(oq):

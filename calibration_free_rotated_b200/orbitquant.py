@@ -400,6 +400,15 @@ def _launch(fn, index, stream, *args):
         _check(rc)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor in the memory of the stream that will use it (None: the current one), so that
+    it is not handed to another stream's work while this one's is under way."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _rows(name, t, index, heads, d, T=None, dtype=None):
     """Strides (token, head) of rows [T, heads, d] on device `index` (heads, d, T,
     dtype: None for any)."""
@@ -439,7 +448,7 @@ def rope_apply(rope: Rope, x: torch.Tensor, pos: torch.Tensor, out=None, inverse
     T, heads, d = x.shape
     dtype = x.dtype
     if out is None:
-        out = torch.empty((T, heads, d), dtype=dtype, device=x.device)
+        out = _empty((T, heads, d), dtype, x.device, stream)
     so = _rows("out", out, index, heads, d, T, dtype)
     if pos.dtype is not _I32 or pos.shape != (T, rope.n_axes) or pos.get_device() != index or not pos.is_contiguous():
         raise ValueError(f"pos must be contiguous int32 [{T}, {rope.n_axes}] on x's device "
@@ -470,7 +479,7 @@ def cache_read(cache: KVCache, cu: torch.Tensor, first: torch.Tensor, table: tor
     if k is None or v is None:
         if k is not None or v is not None or T is None:
             raise ValueError("pass k and v, or T")
-        k, v = (torch.empty((T, cache.heads, cache.d), dtype=dtype, device=cache.device) for _ in range(2))
+        k, v = (_empty((T, cache.heads, cache.d), dtype, cache.device, stream) for _ in range(2))
     index, dtype = cache._index, k.dtype
     _rows("k", k, index, cache.heads, cache.d, T)
     _rows("v", v, index, cache.heads, cache.d, k.shape[0], dtype)
@@ -496,12 +505,12 @@ def cache_attention(cache: KVCache, q: torch.Tensor, cu: torch.Tensor, lens: tor
     sq = _rows("q", q, index, None, cache.d)
     T, heads, d = q.shape
     if out is None:
-        out = torch.empty((T, heads, d), dtype=dtype, device=cache.device)
+        out = _empty((T, heads, d), dtype, cache.device, stream)
     so = _rows("out", out, index, heads, d, T, dtype)
     cu_p, at_p, B, table_p, width = _batch(cache, cu, "lens", lens, table)
     if workspace is None:
         need = _lib.oq_cache_attention_workspace_bytes(cache._ref, T, B, heads)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=cache.device)
+        workspace = _empty((need,), torch.uint8, cache.device, stream)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on q's device")
     _launch(_lib.oq_cache_attention, index, stream, cache._ref, None if rpbh is None else rpbh._h, q.data_ptr(), sq[0],

@@ -629,6 +629,29 @@ def test_two_calls_at_once(oq, n):
             assert torch.equal(o, want[j])
 
 
+def test_memory_made_for_another_stream_is_its_own(oq):
+    """Without `out` and `workspace`, what a call on a given stream makes comes from that stream's memory."""
+    rng = np.random.default_rng(36)
+    bt = Batch(rng, [3, 1], [50, 700], 16)
+    cache = filled(oq, rng, bt, 2, 64, None)
+    q, rope, pos = rows(rng, (4, 4, 64), "bf16"), oq.Rope((64,)), ints([[0], [1], [2], [3]])
+    cu, total, table = ints(bt.cu), ints(bt.total), ints(bt.table)
+    want = oq.cache_attention(cache, oq.rope_apply(rope, q, pos), cu, total, table)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    turned = oq.rope_apply(rope, q, pos, stream=side)
+    got = oq.cache_attention(cache, turned, cu, total, table, stream=side)
+    k, _ = oq.cache_read(cache, cu, ints([0, 0]), table, T=4, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    blocks = [(s["address"], s["address"] + s["total_size"]) for s in torch.cuda.memory_snapshot()
+              if s["stream"] == side.cuda_stream]
+    for t in (turned, got, k):
+        assert any(a <= t.data_ptr() < b for a, b in blocks)
+    need = oq.cache_attention_workspace_bytes(cache, 4, 2, 4)
+    assert sum(b - a for a, b in blocks) >= need
+
+
 _CHILD = r"""
 import sys
 import torch

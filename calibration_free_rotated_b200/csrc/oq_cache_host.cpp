@@ -11,18 +11,22 @@ using namespace oq;
 
 namespace {
 
+// Most rows, and most tokens of a sequence: the kernels look a few tiles ahead in 32-bit
+// places.
+constexpr long long kMost = 0x7FFF0000ll;
+
 int rope_table(oq_rope_t r, const unsigned long long** freq, const uint8_t** axis) {
   int dev;
   if (int rc = current_device(&dev)) return rc;
   std::lock_guard<std::mutex> lk(r->mu);
   const size_t n = r->freq.size();
   if (!r->dev_table[dev]) {
-    std::vector<unsigned char> t(9 * n);
-    std::memcpy(t.data(), r->freq.data(), 8 * n);
-    std::memcpy(t.data() + 8 * n, r->axis.data(), n);
+    unsigned char t[9 * 256];
+    std::memcpy(t, r->freq.data(), 8 * n);
+    std::memcpy(t + 8 * n, r->axis.data(), n);
     void* p = nullptr;
-    if (int rc = device_alloc(&p, t.size(), "rope table")) return rc;
-    cudaError_t e = cudaMemcpy(p, t.data(), t.size(), cudaMemcpyHostToDevice);
+    if (int rc = device_alloc(&p, 9 * n, "rope table")) return rc;
+    cudaError_t e = cudaMemcpy(p, t, 9 * n, cudaMemcpyHostToDevice);
     if (e != cudaSuccess) {
       cudaFree(p);
       return fail(OQ_ERR_CUDA, "uploading the rope table: %s", cudaGetErrorString(e));
@@ -75,8 +79,9 @@ int check_batch(const oq_kvcache* c, int dtype, int T, const void* cu, const voi
   if (T < 0 || B < 0) return fail(OQ_ERR_ARG, "T and B must be >= 0 (got %d, %d)", T, B);
   if (T == 0 || B == 0) return OQ_OK;
   if (width < 1) return fail(OQ_ERR_ARG, "the page table needs a width >= 1 (got %d)", width);
-  if ((long long)width * c->page > 0x7FFFFFFFll)
-    return fail(OQ_ERR_UNSUPPORTED, "a sequence holds fewer than 2^31 tokens (%d pages of %d)", width, c->page);
+  if (T > kMost) return fail(OQ_ERR_UNSUPPORTED, "T must be at most %lld (got %d)", kMost, T);
+  if ((long long)width * c->page > kMost)
+    return fail(OQ_ERR_UNSUPPORTED, "a sequence holds at most %lld tokens (%d pages of %d)", kMost, width, c->page);
   if (!cu || !at || !table) return fail(OQ_ERR_ARG, "NULL index buffer");
   if (((uintptr_t)cu | (uintptr_t)at | (uintptr_t)table) & 3u)
     return fail(OQ_ERR_ALIGN, "index buffers must be 4-byte aligned");
@@ -164,6 +169,8 @@ int oq_rope_apply(oq_rope_t rope, const void* X, long long x_token, long long x_
   const int pairs = (int)rope->freq.size();
   if (2 * pairs > d) return fail(OQ_ERR_ARG, "%d pairs do not fit into rows of %d", pairs, d);
   if (d % 8 != 0 || d > 512) return fail(OQ_ERR_UNSUPPORTED, "rope needs d %% 8 == 0 and d <= 512 (d=%d)", d);
+  if (T > kMost || heads > 65535)
+    return fail(OQ_ERR_UNSUPPORTED, "rope needs T <= %lld and heads <= 65535 (got %d, %d)", kMost, T, heads);
   if (rope->halves && pairs % 8 != 0)
     return fail(OQ_ERR_UNSUPPORTED, "the halves layout needs pairs %% 8 == 0 (pairs=%d)", pairs);
   if (T == 0 || heads == 0) return OQ_OK;
@@ -243,8 +250,8 @@ int oq_cache_attention(const oq_kvcache* cache, oq_rpbh_t r, const void* Q, long
     return fail(OQ_ERR_ARG, "query heads (%d) must be a multiple of the cache's (%d)", heads, cache->heads);
   if (!std::isfinite(scale)) return fail(OQ_ERR_ARG, "scale must be finite");
   if (T == 0 || B == 0) return OQ_OK;
-  if ((long long)T * heads > 0x7FFFFFFFll)
-    return fail(OQ_ERR_UNSUPPORTED, "T * heads must be below 2^31 (%d, %d)", T, heads);
+  if ((long long)T * heads > kMost)
+    return fail(OQ_ERR_UNSUPPORTED, "T * heads must be at most %lld (%d, %d)", kMost, T, heads);
   if (int rc = check_rows("Q", Q, q_token, q_head, 2)) return rc;
   if (int rc = check_rows("O", O, o_token, o_head, 2)) return rc;
   if (Q == O) return fail(OQ_ERR_ARG, "O may not be Q");

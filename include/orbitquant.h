@@ -350,7 +350,9 @@ OQ_API int oq_linear_noalloc(oq_rpbh_t r, oq_codebook_t cb_a, oq_codebook_t cb_w
  * contiguous; `*_token` and `*_head` are the strides, in elements, between
  * tokens and between heads (slices of a fused [T][heads][d] tensor need no
  * copy).  Base pointers are 16-byte aligned and strides multiples of 16 bytes
- * (OQ_ERR_ALIGN), so that rows are too.
+ * (OQ_ERR_ALIGN), so that rows are too.  Most sizes: T and the tokens of a
+ * sequence 0x7FFF0000 (attention: T * heads too), heads 65535
+ * (OQ_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 enum { OQ_BF16 = 0, OQ_FP16 = 1, OQ_FP32 = 2 };
 typedef struct oq_rope_s* oq_rope_t;
@@ -392,8 +394,8 @@ OQ_API int oq_rope_apply(oq_rope_t rope, const void* X, long long x_token, long 
  * ... (int32, one row of `width` entries for each sequence); entries behind its
  * last page are not read.  A page may serve several sequences for reading
  * (a shared prefix); one that is written to belongs to one sequence.
- * heads >= 1, page in {16, 32, 64, 128}, d in {64, 128}; n_pages * page and
- * width * page below 2^31 (OQ_ERR_UNSUPPORTED otherwise).  Pages need no
+ * heads >= 1, page in {16, 32, 64, 128}, d in {64, 128}; n_pages * page below
+ * 2^31, width * page at most 0x7FFF0000 (OQ_ERR_UNSUPPORTED otherwise).  Pages need no
  * preparation; a key scale of 0 marks a page as empty (attention skips it).
  * ------------------------------------------------------------------------- */
 typedef struct {

@@ -127,6 +127,24 @@ def test_rope_arguments(oq):
             oq.Rope(**bad)
 
 
+def test_sizes_at_the_end_of_32_bits(oq):
+    """What the kernels' 32-bit places could not hold is refused before a launch."""
+    L, c, most, many = oq.lib(), struct(oq), 0x7FFF0000, 0x7FFFFFFF
+    r = oq.Rope((16, 24, 24))
+
+    def apply(T, heads):
+        return L.oq_rope_apply(r.handle, BASE, 64, 64, 2 * BASE, 64, 64, 0, T, heads, 64, BASE, 0, None)
+
+    assert apply(most + 1, 1) == oq.OQ_ERR_UNSUPPORTED and apply(many, 1) == oq.OQ_ERR_UNSUPPORTED
+    assert apply(1, 65536) == oq.OQ_ERR_UNSUPPORTED and apply(1, many) == oq.OQ_ERR_UNSUPPORTED
+    for T, width in ((many, 1), (most + 1, 1), (1, most // 16 + 1), (1, many)):
+        assert L.oq_cache_write(c, None, BASE, 64, 64, BASE, 64, 64, 0, T, BASE, BASE, 1, BASE, width,
+                                None) == oq.OQ_ERR_UNSUPPORTED
+        assert L.oq_cache_read(c, None, BASE, BASE, 0, T, BASE, BASE, 1, BASE, width, None) == oq.OQ_ERR_UNSUPPORTED
+        assert L.oq_cache_attention(c, None, BASE, 256, 64, 2 * BASE, 256, 64, 0, 4, T, BASE, BASE, 1, BASE, width, 1,
+                                    1.0, BASE, 1 << 60, None) == oq.OQ_ERR_UNSUPPORTED
+
+
 def test_binding_checks_tensors(oq):
     """Shapes, types and devices that the library cannot see from pointers."""
     c = oq.KVCache(2, 1, 64, 16, device="cpu")

@@ -2,36 +2,39 @@
 // whole images): bound by the tensor cores and what feeds them.
 //
 // The same sums as oq_cattn.cu, on tcgen05: a CTA (one on each SM) takes 256 query
-// rows as two tiles of 128 and walks KT keys a step.  Four roles:
-//   warps 0..7   four a tile, one thread a row: scores from TMEM, running maximum
-//                and sum, weights back into TMEM.
-//   warps 8, 9   expand the step's key codes to fp16 (exact) into the K-major
+// rows as two tiles of 128 and walks KT keys a step.  Three roles:
+//   warps 8..11  expand the step's codes to fp16 (exact) into the K-major
 //                128-byte-swizzled layout of the tensor cores' operands, once for
-//                both tiles, with the next step's codes already in registers.
-//   warps 10..13 the same with the values, transposed by byte permutes.
-//   warps 14, 15 issue the products, one for each tile.
-// TMEM, all 512 columns: for each tile two steps' scores (64 columns each, whose
-// first half the weights take over as the left operand of the sum) and the sum (D
-// columns), which stays until the end.  So the scores of a step are there before the
-// weights of the one before it are done, and neither the rows' threads nor the
-// tensor cores wait for a round trip of the other.  The turned queries (fp16) are
+//                both tiles: the keys as they lie, the values transposed by byte
+//                permutes, with the codes of what comes next already in registers.
+//   warps 0..7   four a tile, one thread a row: scores from TMEM, running maximum
+//                and sum, weights back into TMEM in two halves, so that the first
+//                half's products run beside the second half's exponentials.
+//   warp 12      issues the products; one tile's run beside the other tile's
+//                exponentials.
+// TMEM, all 512 columns: each tile's scores (KT columns), whose first half the
+// weights take over (the left operand of the sum), and each tile's sum (D
+// columns), which stays until the end.  The turned queries (fp16) are
 // shared-memory operands.  The turns themselves are products too: the rows as they
 // come times the matrix Pi (entries 0, 1, -1: exact), and at the end the sums, as
-// two terms of the tensor's type (2^-17 and better), times its transpose; the matrix
-// is written into the values' place when it is needed.  (Butterflies on the 256 rows
-// took 33 thousand clocks an item, a tenth of a long one.)
+// two terms of the tensor's type (2^-17 and better), times its transpose; the
+// matrix is written into the values' place when it is needed.  (Butterflies on the
+// 256 rows took 33 thousand clocks an item, a tenth of a long one.)
 //
-// What bounds it, at 4608 x 4608 rows, D = 128, 24 heads (330 us, 790 TFLOP/s; 31200
-// + 1560 keys for 1560 rows, 12 heads: 395 us): a step of 64 keys takes 2150 clocks, of
-// which the exponentials take 1024 (16 a clock), the tensor cores 1330 (scores of 64
-// keys read 6 KB of operands for 32 clocks of products), the issue slots 60 %; the
-// rows' threads never wait, but two warps a scheduler leave gaps.  An item's beginning
-// and end take 25 thousand clocks (D = 64: 15), a fifth of the first example.
-// What was tried beside it (times of the two examples): four warps that expand keys
-// and then values, 335 / 449 (they were the last to be done); 18 warps of 96
-// registers, 357 / 420 (spills); two threads a row, 24 warps, 359 / 460; 128 keys a
-// step in two halves with one buffer of scores, 371 / 447; one product warp 12 us
-// more; a product warp whose operands' addresses are not warp-uniform, 35 us more.
+// What bounds it (4608 x 4608 rows, D = 128, 24 heads, bf16: 337 us, 775 TFLOP/s, in
+// calls one by one 345; 31200 + 1560 keys for 1560 rows, 12 heads: 390 and 418;
+// chunks of up to 511 rows, D = 64, fp16, causal: 83): 64 keys take 2150 clocks, of which
+// the exponentials take 1024 (16 a clock), the tensor cores 1100, the issue slots
+// 50 to 60 %.  Without the exponentials the first example takes 5 % less, without the
+// expansion 12 %, without the weights altogether 15 %, with a quarter of the products
+// 3 %: no single part is left to mend.  An item's beginning and end take 25 thousand
+// clocks (D = 64: 15), a fifth of the first example.
+// Tried beside it (the first two examples, us): 64 keys a step, with scores a step
+// ahead, warps of their own for keys (2) and values (4), and a product warp for each
+// tile, 330 and 395 (one by one 346 and 427, the chunks 87); the same with four warps
+// for keys and values, 335 and 449; with two threads a row (24 warps), 359 and 460;
+// this one with a product warp for each tile and six expanding warps, 371 and 447; two
+// CTAs an SM of one tile each, 1.9 times as long.
 //
 // Scales: as in oq_cattn.cu the running maximum is taken over score + ev, so
 // the weights carry their page's value exponent; groups of 16 tokens (no page is
@@ -40,8 +43,8 @@
 //
 // fp16 queries keep a second term: the turn rounds them to 2^-12, which would
 // show beside an fp16 result, so what the first operand leaves out goes into a
-// second one and the scores take both.  (At D = 128 its 64 KB leave room for two
-// stages of keys and values instead of three.)
+// second one and the scores take both.  (At D = 128 that operand's 32 KB leave
+// room for 64 keys a step instead of 128.)
 //
 // Every wait is bounded (~1 s); one that gives up records OQ_ERR_TIMEOUT and
 // raises a flag that lets all others return at once, and the CTA still reaches
@@ -58,11 +61,9 @@ namespace {
 
 using namespace cattn;
 
-constexpr int kThreads = 512, kRows = 256, kTileRows = 128;
+constexpr int kThreads = 416, kRows = 256, kTileRows = 128;
 constexpr int kTmem = 512, kColS = 0, kColO = 256;  // a tile's columns begin 128 further on
-// Units (steps of 64 keys) of an item's beginning and end: 7 (D = 64) to 12 by the
-// clock.  With 4 a batch of ragged chunks took 100 us, with 8 89, with 12 87.
-constexpr int kStart = 12;
+constexpr int kStart = 4;  // units of an item's beginning and end
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -314,27 +315,23 @@ __device__ __forceinline__ uint4 turn_chunk(const uint16_t* inv, int row, int c,
 
 template <int D, bool TWO>
 struct Smem {
-  static constexpr int KT = 64;                              // keys of a step
-  static constexpr int NST = TWO && D == 128 ? 2 : 3;        // stages of keys, and of values
+  static constexpr int KT = 128;                             // keys of a step
+  static constexpr int VST = TWO && D == 128 ? 1 : 2;        // stages of values
   static constexpr int kOperand = 2 * D * KT;                // bytes of a stage of keys, of values
   static constexpr int kTileQ = kTileRows * D * 2;           // of a tile's queries
-  static constexpr int kKeys = 0, kValues = NST * kOperand, kQuery = 2 * NST * kOperand;
+  static constexpr int kKeys = 0, kValues = kOperand, kQuery = (1 + VST) * kOperand;
   static constexpr int kLow = kQuery + 2 * kTileQ;           // the queries' second term
-  static constexpr int kScales = kLow + (TWO ? 2 * kTileQ : 0);             // [8][KT / 16] (key scale, ev, 2^-ev)
-  static constexpr int kInverse = kScales + 8 * (KT / 16) * 16;             // [D] 16 bits: see invert
+  static constexpr int kScales = kLow + (TWO ? 2 * kTileQ : 0);             // [2][KT / 16] (key scale, ev, 2^-ev)
+  static constexpr int kInverse = kScales + 2 * (KT / 16) * 16;             // [D] 16 bits: see invert
   static constexpr int kStat = kInverse + 2 * D;                            // [rows] maximum, sum
   static constexpr int kBars = kStat + kRows * 8;
-  static constexpr int kTotal = kBars + 256;
+  static constexpr int kTotal = kBars + 192;
   static constexpr int kAlloc = kTotal + 1024;  // room to align the base
-  // Outside the steps: the matrix in the values' first stages; the sums' second terms
-  // in the queries' second terms' place, or the keys' first stages and what is left of
-  // the keys' and values' last.
+  // Outside the steps: the matrix in the values' first stage; the sums' second terms
+  // in the queries' second terms' place, or the keys' and the values' second stage.
   static constexpr int kMatrix = kValues;
-  static constexpr int kSumLow0 = TWO ? kLow : kKeys;
-  static constexpr int kSumLow1 = TWO ? kLow + kTileQ : kKeys + kTileQ;  // (two terms in a row: the matrix follows)
-  static constexpr int kMatrixOut = TWO ? kValues : kKeys + 2 * kTileQ;
-  static_assert(D * D * 2 <= NST * kOperand, "the matrix in the values' place");
-  static_assert(kMatrixOut + D * D * 2 <= kQuery, "the sums' second terms and the matrix before the queries");
+  static constexpr int kSumLow0 = TWO ? kLow : kKeys, kSumLow1 = TWO ? kLow + kTileQ : kValues + kOperand;
+  static_assert(D * D * 2 <= kOperand && kTileQ <= kOperand, "what stands in the operands' place");
   static_assert(kRows * D * 4 <= kScales, "the rows' sums stand in the operands' place at the end");
   static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
 };
@@ -342,7 +339,7 @@ struct Smem {
 template <typename T, int D, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Args a) {
   using S = Smem<D, TWO>;
-  constexpr int KT = S::KT, NST = S::NST, LPR = D / 8;
+  constexpr int KT = S::KT, HK = KT / 2, LPR = D / 8, VST = S::VST;
   extern __shared__ unsigned char sm_raw[];
   chain_wait();
   unsigned char* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
@@ -352,23 +349,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   float2* row_stat = reinterpret_cast<float2*>(sm + S::kStat);
   float4* scales = reinterpret_cast<float4*>(sm + S::kScales);
   const uint32_t bars = base + S::kBars;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + S::kBars + 240);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 244);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + S::kBars + 160);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 164);
   auto bar = [&](int i) { return bars + 8u * i; };
-  // of the stages (K_FULL + stage); of the two tiles and their buffers (S_FULL + 2 w + buffer)
-  constexpr int K_FULL = 0, K_EMPTY = 3, V_FULL = 6, V_EMPTY = 9, S_FULL = 12, P_FULL = 16, O_FULL = 20, TURN = 22;
+  // of the two tiles (S_FULL + w) and of a tile's halves (P_FULL + 2 w + half)
+  constexpr int K_FULL = 0, K_EMPTY = 1, V_FULL = 2, V_EMPTY = 4, S_FULL = 6, P_FULL = 8, HALF = 12, O_FULL = 14, TURN = 16;
 
   if (tid == 0) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(bar(K_FULL + i), 2), mbar_init(bar(K_EMPTY + i), 2);  // emptied by both tiles
-      mbar_init(bar(V_FULL + i), 4), mbar_init(bar(V_EMPTY + i), 2);
+    mbar_init(bar(K_FULL), 4), mbar_init(bar(K_EMPTY), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(V_FULL + i), 4), mbar_init(bar(V_EMPTY + i), 1);
+      mbar_init(bar(S_FULL + i), 1), mbar_init(bar(HALF + i), 1), mbar_init(bar(O_FULL + i), 1);
+      mbar_init(bar(P_FULL + 2 * i), 4), mbar_init(bar(P_FULL + 2 * i + 1), 4);
+      mbar_init(bar(TURN + i), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar(S_FULL + i), 1), mbar_init(bar(P_FULL + i), 4);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(O_FULL + i), 1), mbar_init(bar(TURN + i), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 14) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                  "r"(kTmem)
                  : "memory");
@@ -387,9 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   int4 desc = make_int4(0, 0, 0, 0);
   int b = sh.b;
   long long into = sh.into;
-  // the barriers' phases: steps of the keys, items of each tile, turns
-  uint32_t steps = 0, tile_items[2] = {0, 0}, turns = 0;
-  uint32_t tile_phase[2][2] = {{0, 0}, {0, 0}};  // of each tile's two buffers
+  // the barriers' phases: steps of the keys, of each tile, items of each tile, turns
+  uint32_t steps = 0, tile_steps[2] = {0, 0}, tile_items[2] = {0, 0}, turns = 0;
   const int l = tid % LPR;
   const int plog = 31 - __clz(a.c.page);
 
@@ -438,186 +435,177 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    const int* table = a.table + (size_t)b * a.width;
-    auto page_at = [&](int tok) { return tok < keys ? table[tok >> plog] : 0; };
-    auto row_at = [&](int page, int tok) -> size_t {  // row of codes of a token (some row where there is none)
-      if (page < 0 || page >= a.c.n_pages) page = 0;
-      return (((size_t)page * a.c.heads + h) << plog) + (tok & (a.c.page - 1));
-    };
-    auto make_matrix = [&]() {
+
+    if (warp >= 8 && warp < 12) {
+      // ---- expanding the codes ----
+      // Keys: eight lanes beside one another have two rows' 16-byte pieces of one
+      // 128-byte block, which lie in different banks.  Values: a lane takes eight
+      // tokens and VB bytes of each; eight lanes beside one another have eight token
+      // groups, whose chunks lie in different banks.
+      const int ct = tid - 256;
+      constexpr int KP = (KT / 32) * (D / 64);         // 16-byte pieces of keys of a lane
+      constexpr int VB = KT * D / 1024, VW = VB / 4;   // bytes and words of a token's values
+      const int kr = ct >> 2, kc = ct & 3;
+      const int vt = 8 * (warp & 1) + (lane & 7);
+      const int vd = (((warp - 8) >> 1) * 4 + (lane >> 3)) * VB;
+      const int* table = a.table + (size_t)b * a.width;
+      auto row_at = [&](int tok) -> size_t {  // row of codes of a token (some row where there is none)
+        int page = 0;
+        if (tok < keys) {
+          page = table[tok >> plog];
+          if (page < 0 || page >= a.c.n_pages) page = 0;
+        }
+        return (((size_t)page * a.c.heads + h) << plog) + (tok & (a.c.page - 1));
+      };
+      uint32_t code[4 * KP];  // of the keys or the values, whichever comes next
+      static_assert(8 * VW == 4 * KP, "as many codes either way");
+      auto load_k = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < KT / 32; ++i) {
+          const int8_t* p = a.c.k + row_at(tok0 + t * KT + 32 * i + kr) * D + 16 * kc;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + 64 * j);
+            uint32_t* to = code + 4 * (i * (D / 64) + j);
+            to[0] = w.x, to[1] = w.y, to[2] = w.z, to[3] = w.w;
+          }
+        }
+      };
+      auto load_v = [&](int t) {
+        const int8_t* p = a.c.v + row_at(tok0 + t * KT + 8 * vt) * D + vd;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (VW == 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + j * D);
+            code[4 * j] = w.x, code[4 * j + 1] = w.y, code[4 * j + 2] = w.z, code[4 * j + 3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(p + j * D);
+            code[2 * j] = w.x, code[2 * j + 1] = w.y;
+          }
+        }
+      };
+      float2 sc = make_float2(0.0f, 1.0f);
+      auto load_scales = [&](int t) {  // a thread for each group of 16 tokens
+        const int tok = tok0 + t * KT + 16 * ct;
+        sc = make_float2(0.0f, 1.0f);  // a key scale of 0: no keys
+        if (tok < keys) {
+          const int page = table[tok >> plog];
+          if (page >= 0 && page < a.c.n_pages) {
+            const size_t ph = (size_t)page * a.c.heads + h;
+            sc = make_float2(a.c.ks[ph], a.c.vs[ph]);
+          } else {
+            bad_index(a.status);
+          }
+        }
+      };
+      load_k(0);
+      if (ct < KT / 16) load_scales(0);
       if (turned)
-        for (int c = tid - 256; c < D * LPR; c += kThreads - 256) {
+        for (int c = tid - 256; c < D * LPR; c += 160) {
           const uint4 w = turn_chunk<false>(inv, c / LPR, c % LPR, a.r.h, one);
           sts128(base + S::kMatrix + ((c % LPR) >> 3) * (D * 128) + (c / LPR) * 128 + (((c & 7) ^ (c / LPR & 7)) << 4), w.x, w.y,
                  w.z, w.w);
         }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncthreads();
-    };
-    if (warp >= 8 && warp < 10) {
-      // ---- expanding the keys ----
-      // Eight lanes beside one another have two rows' 16-byte pieces of one 128-byte
-      // block, which lie in different banks.  The codes are read a step ahead, their
-      // pages two.
-      const int ct = tid & 63, kr = ct >> 2, kc = ct & 3;
-      uint32_t code[KT / 16][D / 64][4];
-      int page[KT / 16], scale_page = 0;
-      float2 sc = make_float2(0.0f, 1.0f);
-      auto load_pages = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < KT / 16; ++i) page[i] = page_at(tok0 + t * KT + 16 * i + kr);
-        if (ct < KT / 16) scale_page = page_at(tok0 + t * KT + 16 * ct);
-      };
-      auto load = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < KT / 16; ++i) {
-          const int8_t* p = a.c.k + row_at(page[i], tok0 + t * KT + 16 * i + kr) * D + 16 * kc;
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            const uint4 x = *reinterpret_cast<const uint4*>(p + 64 * j);
-            code[i][j][0] = x.x, code[i][j][1] = x.y, code[i][j][2] = x.z, code[i][j][3] = x.w;
-          }
-        }
-        if (ct < KT / 16) {  // a thread for each group of 16 tokens
-          sc = make_float2(0.0f, 1.0f);  // a key scale of 0: no keys
-          if (tok0 + t * KT + 16 * ct < keys) {
-            if (scale_page >= 0 && scale_page < a.c.n_pages) {
-              const size_t ph = (size_t)scale_page * a.c.heads + h;
-              sc = make_float2(a.c.ks[ph], a.c.vs[ph]);
-            } else {
-              bad_index(a.status);
-            }
-          }
-        }
-      };
-      load_pages(0);
-      load(0);
-      load_pages(1);
-      make_matrix();
-      uint32_t st = steps % NST, ph = steps / NST & 1u;
       for (int t = 0; t < take; ++t) {
-        wait_bounded(bar(K_EMPTY + st), ph ^ 1u, abort_flag, a.status);
+        const uint32_t it = steps + t;
+        wait_bounded(bar(K_EMPTY), (it & 1u) ^ 1u, abort_flag, a.status);
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < KT / 16; ++i) {
-          const int n = 16 * i + kr;
+        for (int i = 0; i < KT / 32; ++i) {
+          const int n = 32 * i + kr;
 #pragma unroll
           for (int j = 0; j < D / 64; ++j)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {  // eight codes: one 16-byte chunk
-              const uint32_t x0 = code[i][j][2 * u] ^ 0x80808080u, x1 = code[i][j][2 * u + 1] ^ 0x80808080u;
-              sts128(base + S::kKeys + st * S::kOperand + j * (KT * 128) + n * 128 + (((2 * kc + u) ^ (n & 7)) << 4),
-                     bytes2(x0, 0x4140), bytes2(x0, 0x4342), bytes2(x1, 0x4140), bytes2(x1, 0x4342));
+              const uint32_t* w = code + 4 * (i * (D / 64) + j) + 2 * u;
+              const uint32_t w0 = w[0] ^ 0x80808080u, w1 = w[1] ^ 0x80808080u;
+              sts128(base + S::kKeys + j * (KT * 128) + n * 128 + (((2 * kc + u) ^ (n & 7)) << 4), bytes2(w0, 0x4140),
+                     bytes2(w0, 0x4342), bytes2(w1, 0x4140), bytes2(w1, 0x4342));
             }
         }
+        load_v(t);
         if (ct < KT / 16) {
           const int ev = min(max(scale_exp(sc.y), -126), 126);
-          scales[((steps + t) & 7u) * (KT / 16) + ct] = make_float4(sc.x, (float)ev, pow2(-ev), 0.0f);
+          scales[(it & 1u) * (KT / 16) + ct] = make_float4(sc.x, (float)ev, pow2(-ev), 0.0f);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(K_FULL + st));
-        if (t + 1 < take) {
-          load(t + 1);
-          load_pages(t + 2);
+        if (lane == 0) mbar_arrive(bar(K_FULL));
+        if (t + 1 < take && ct < KT / 16) load_scales(t + 1);
+
+        const uint32_t st = it % VST;
+        if (t == 0 && turned) {  // the matrix stands in the values' place
+          wait_bounded(bar(TURN), turns & 1u, abort_flag, a.status);
+          wait_bounded(bar(TURN + 1), turns & 1u, abort_flag, a.status);
         }
-        st = st + 1 == NST ? 0 : st + 1, ph ^= st == 0;
-      }
-    } else if (warp >= 10 && warp < 14) {
-      // ---- expanding the values ----
-      // A lane takes eight tokens and VB bytes of each; eight lanes beside one another
-      // have eight token groups, whose chunks lie in different banks.
-      constexpr int VB = KT * D / 1024, VW = VB / 4;  // bytes and words of a token's values
-      const int vt = lane & 7, vd = ((warp - 10) * 4 + (lane >> 3)) * VB;
-      uint32_t code[8 * VW];
-      int page = 0;
-      auto load_page = [&](int t) { page = page_at(tok0 + t * KT + 8 * vt); };
-      auto load = [&](int t) {
-        const int8_t* p = a.c.v + row_at(page, tok0 + t * KT + 8 * vt) * D + vd;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if constexpr (VW == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(p + j * D);
-            code[2 * j] = x.x, code[2 * j + 1] = x.y;
-          } else {
-            code[j] = *reinterpret_cast<const uint32_t*>(p + j * D);
-          }
-        }
-      };
-      load_page(0);
-      load(0);
-      load_page(1);
-      make_matrix();
-      if (turned) {  // the matrix stands in the values' place
-        wait_bounded(bar(TURN), turns & 1u, abort_flag, a.status);
-        wait_bounded(bar(TURN + 1), turns & 1u, abort_flag, a.status);
-      }
-      uint32_t st = steps % NST, ph = steps / NST & 1u;
-      for (int t = 0; t < take; ++t) {
-        wait_bounded(bar(V_EMPTY + st), ph ^ 1u, abort_flag, a.status);
+        wait_bounded(bar(V_EMPTY + st), ((it / VST) & 1u) ^ 1u, abort_flag, a.status);
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < VW; ++i) {
+        for (int w = 0; w < VW; ++w) {
           uint32_t o[4][4];  // [coordinate][pair of tokens]
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t x0 = code[VW * (2 * q) + i] ^ 0x80808080u, x1 = code[VW * (2 * q + 1) + i] ^ 0x80808080u;
+            const uint32_t x0 = code[VW * (2 * q) + w] ^ 0x80808080u, x1 = code[VW * (2 * q + 1) + w] ^ 0x80808080u;
             const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
             o[0][q] = bytes2(lo, 0x4140), o[1][q] = bytes2(lo, 0x4342);
             o[2][q] = bytes2(hi, 0x4140), o[3][q] = bytes2(hi, 0x4342);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int d = vd + 4 * i + k;
-            sts128(base + S::kValues + st * S::kOperand + d * 128 + ((vt ^ (d & 7)) << 4), o[k][0], o[k][1], o[k][2], o[k][3]);
+            const int d = vd + 4 * w + k;
+            sts128(base + S::kValues + st * S::kOperand + (vt >> 3) * (D * 128) + d * 128 + (((vt & 7) ^ (d & 7)) << 4),
+                   o[k][0], o[k][1], o[k][2], o[k][3]);
           }
         }
+        if (t + 1 < take) load_k(t + 1);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(V_FULL + st));
-        if (t + 1 < take) {
-          load(t + 1);
-          load_page(t + 2);
-        }
-        st = st + 1 == NST ? 0 : st + 1, ph ^= st == 0;
       }
-    } else if (warp >= 14) {
+    } else if (warp == 12) {
       // ---- products: a tile's sum, then its next scores, while the other tile's weights are made ----
-      make_matrix();
-      const int w = warp - 14;
+      if (turned)
+        for (int c = tid - 256; c < D * LPR; c += 160) {
+          const uint4 w = turn_chunk<false>(inv, c / LPR, c % LPR, a.r.h, one);
+          sts128(base + S::kMatrix + ((c % LPR) >> 3) * (D * 128) + (c / LPR) * 128 + (((c & 7) ^ (c / LPR & 7)) << 4), w.x, w.y,
+                 w.z, w.w);
+        }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();
+      const uint64_t md = desc_sw128(base + S::kMatrix);
       if (turned) {
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t qd = desc_sw128(base + S::kQuery + w * S::kTileQ), md = desc_sw128(base + S::kMatrix);
-          if (w < tiles) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tmem + kColS + 128 * w, qd + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
-                     md + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), idesc_of<T, D>(), k > 0);
+          for (int w = 0; w < 2; ++w) {
+            const uint64_t qd = desc_sw128(base + S::kQuery + w * S::kTileQ);
+            if (w < tiles) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(tmem + kColS + 128 * w, qd + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
+                       md + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), idesc_of<T, D>(), k > 0);
+            }
+            commit(bar(TURN + w));
           }
-          commit(bar(TURN + w));
         }
         __syncwarp();
       }
-      asm volatile("bar.sync 1, 320;" ::: "memory");  // with the rows' warps: the queries stand
-      const uint32_t u_w = uniform((uint32_t)w), u_base = uniform(base), u_steps = uniform(steps);
-      const uint32_t u_tmem = uniform(tmem) + 128 * u_w;
-      const int my_take = (int)uniform((uint32_t)(w ? tile_take[1] : tile_take[0]));
-      const int other_take = (int)uniform((uint32_t)(w ? tile_take[0] : tile_take[1]));
-      const uint32_t phase0 = uniform(w ? tile_phase[1][0] : tile_phase[0][0]);
-      const uint32_t phase1 = uniform(w ? tile_phase[1][1] : tile_phase[0][1]);
-      const uint32_t u_bars = u_base + S::kBars;
+      asm volatile("bar.sync 1, 288;" ::: "memory");  // with the rows' warps: the queries stand
+      const uint32_t u_base = uniform(base), u_tmem = uniform(tmem), u_steps = uniform(steps), u_bars = u_base + S::kBars;
+      const int u_take = (int)uniform((uint32_t)take);
+      const int takes[2] = {(int)uniform((uint32_t)tile_take[0]), (int)uniform((uint32_t)tile_take[1])};
+      const uint32_t phase[2] = {uniform(tile_steps[0]), uniform(tile_steps[1])};
       auto u_bar = [&](int i) { return u_bars + 8u * i; };
-      const uint64_t kd0 = desc_sw128(u_base + S::kKeys), vd0 = desc_sw128(u_base + S::kValues);
-      const uint64_t qd = desc_sw128(u_base + S::kQuery + u_w * S::kTileQ), ld = desc_sw128(u_base + S::kLow + u_w * S::kTileQ);
-      uint32_t ks = u_steps % NST, kph = u_steps / NST & 1u, vs = ks, vph = kph;  // the next stages, their phases
-      auto scores = [&](int t) {  // of step t into the tile's buffer t % 2
-        wait_bounded(u_bar(K_FULL + ks), kph, abort_flag, a.status);
+      const uint64_t kd = desc_sw128(u_base + S::kKeys), vd0 = desc_sw128(u_base + S::kValues);
+      const uint64_t qd0 = desc_sw128(u_base + S::kQuery), ld0 = desc_sw128(u_base + S::kLow);
+      auto scores = [&](int w, int t) {
+        if (t == 0 || w == 0 || takes[0] <= t) wait_bounded(u_bar(K_FULL), (u_steps + t) & 1u, abort_flag, a.status);
         __syncwarp();
         tc_fence_after();
-        const uint32_t to = u_tmem + kColS + 64 * (t & 1), full = u_bar(S_FULL + 2 * u_w + (t & 1)), empty = u_bar(K_EMPTY + ks);
-        const uint64_t kd = kd0 + (uint64_t)(ks * (S::kOperand / 16));
-        const bool alone = t >= other_take;  // then this warp stands for the tile that takes no part, too
+        const uint64_t qd = qd0 + (uint64_t)(w * (S::kTileQ / 16)), ld = ld0 + (uint64_t)(w * (S::kTileQ / 16));
+        const uint32_t to = u_tmem + kColS + 128 * w, full = u_bar(S_FULL + w);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
@@ -630,32 +618,53 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                      kd + (uint64_t)((k >> 2) * (KT * 8) + (k & 3) * 2), idesc<KT>(), 1u);
           }
           commit(full);
-          commit(empty);
-          if (alone) commit(empty);
         }
         __syncwarp();
-        ks = ks + 1 == NST ? 0 : ks + 1, kph ^= ks == 0;
       };
-      for (int t = 0; t < min(2, my_take); ++t) scores(t);
-      for (int t = 0; t < my_take; ++t) {
-        wait_bounded(u_bar(V_FULL + vs), vph, abort_flag, a.status);
-        wait_bounded(u_bar(P_FULL + 2 * u_w + (t & 1)), ((t & 1 ? phase1 : phase0) + (t >> 1)) & 1u, abort_flag, a.status);
+      auto keys_done = [&]() {
+        const uint32_t empty = u_bar(K_EMPTY);
+        if (elect_one()) commit(empty);
         __syncwarp();
-        tc_fence_after();
-        const uint64_t vd = vd0 + (uint64_t)(vs * (S::kOperand / 16));
-        const uint32_t to = u_tmem + kColO, from = u_tmem + kColS + 64 * (t & 1), empty = u_bar(V_EMPTY + vs);
-        const uint32_t done = u_bar(O_FULL + u_w);
-        const bool end = t + 1 == my_take, alone = t >= other_take;
-        if (elect_one()) {
+      };
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k) mma_ts<D>(to, from + 8 * k, vd + (uint64_t)(2 * k), t > 0 || k > 0);
-          commit(empty);
-          if (alone) commit(empty);
-          if (end) commit(done);
+      for (int w = 0; w < 2; ++w)
+        if (takes[w] > 0) scores(w, 0);
+      keys_done();
+      for (int t = 0; t < u_take; ++t) {
+        const uint32_t it = u_steps + t, st = it % VST;
+        wait_bounded(u_bar(V_FULL + st), (it / VST) & 1u, abort_flag, a.status);
+        const uint64_t vd = vd0 + (uint64_t)(st * (S::kOperand / 16));
+        const uint32_t empty = u_bar(V_EMPTY + st);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (t < takes[w]) {
+            const uint32_t to = u_tmem + kColO + 128 * w, from = u_tmem + kColS + 128 * w;
+            const uint32_t half = u_bar(HALF + w), done = u_bar(O_FULL + w);
+            const bool end = t + 1 == takes[w];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              wait_bounded(u_bar(P_FULL + 2 * w + hf), (phase[w] + t) & 1u, abort_flag, a.status);
+              __syncwarp();
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int k = hf * (HK / 16); k < (hf + 1) * (HK / 16); ++k)
+                  mma_ts<D>(to, from + 8 * k, vd + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), t > 0 || k > 0);
+                if (hf == 0)
+                  commit(half);
+                else if (end)
+                  commit(done);
+              }
+              __syncwarp();
+            }
+          }
+          if (w == 1) {
+            if (elect_one()) commit(empty);
+            __syncwarp();
+          }
+          if (t + 1 < takes[w]) scores(w, t + 1);
         }
-        __syncwarp();
-        vs = vs + 1 == NST ? 0 : vs + 1, vph ^= vs == 0;
-        if (t + 2 < my_take) scores(t + 2);
+        if (t + 1 < u_take) keys_done();
       }
     } else {
       // ---- weights ----
@@ -664,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       const int w = warp >> 2, tr = tid & (kTileRows - 1);
       const uint32_t tmem_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * w;  // this warp's lanes
       const int my_take = w ? tile_take[1] : tile_take[0];
-      const uint32_t my_phase0 = w ? tile_phase[1][0] : tile_phase[0][0], my_phase1 = w ? tile_phase[1][1] : tile_phase[0][1];
+      const uint32_t my_steps = w ? tile_steps[1] : tile_steps[0];
       const uint32_t my_query = base + S::kQuery + w * S::kTileQ + tr * 128;
       // this thread's row: turned, scaled by a power of two, fp16, back into the operand's place
       float fac = 0.0f;
@@ -731,57 +740,61 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
-      asm volatile("bar.sync 1, 320;" ::: "memory");
+      asm volatile("bar.sync 1, 288;" ::: "memory");
       float top = 0.0f, sum = 0.0f;
       bool none = true;  // no key seen so far: the maximum says nothing
       for (int t = 0; t < my_take; ++t) {
-        const uint32_t buf = t & 1u, ph = ((buf ? my_phase1 : my_phase0) + (t >> 1)) & 1u;
-        wait_bounded(bar(S_FULL + 2 * w + buf), ph, abort_flag, a.status);
+        const uint32_t ph = (my_steps + t) & 1u;
+        wait_bounded(bar(S_FULL + w), ph, abort_flag, a.status);
         __syncwarp();
         tc_fence_after();
-        const float4* sc = scales + ((steps + t) & 7u) * (KT / 16);
-        const uint32_t from = tmem_row + kColS + 64 * buf;
-        const int left = lim - (tok0 + t * KT);  // keys of the step that the row may see
-        const bool whole = __all_sync(0xFFFFFFFFu, left >= KT);
-        // The weights at once, against the maximum so far; in the rare step that
-        // raises it (2^15 and more above, or the first keys of a row) once more
-        // from the scores, which still stand in TMEM.
-        uint32_t p[KT / 2];
-        for (int tries = 0; tries < 2; ++tries) {
-          float mx;
-          const float more = whole ? weigh<KT, false>(from, sc, fac, top, left, p, mx)
-                                   : weigh<KT, true>(from, sc, fac, top, left, p, mx);
-          const bool raise = mx > kRaise || (none && mx > -INFINITY);
-          if (tries > 0 || !__any_sync(0xFFFFFFFFu, raise)) {
-            sum += more;
-            break;
-          }
-          const float up = raise ? mx : 0.0f;
-          const float f = none ? 1.0f : ex2(-up);  // nothing to rescale before the first key
-          top += up;
-          if (raise) none = false;
-          sum *= f;
-          if (t > 0) {  // the last step's products must have been added to the sum in TMEM
-            const uint32_t was = steps + t - 1;
-            wait_bounded(bar(V_EMPTY + was % NST), was / NST & 1u, abort_flag, a.status);
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(tmem_row + kColO + c, o);
-              wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(tmem_row + kColO + c, o);
+        for (int hf = 0; hf < 2; ++hf) {
+          const float4* sc = scales + ((steps + t) & 1u) * (KT / 16) + hf * (HK / 16);
+          const uint32_t from = tmem_row + kColS + HK * hf;
+          const int left = lim - (tok0 + t * KT + HK * hf);  // keys of the half that the row may see
+          const bool whole = __all_sync(0xFFFFFFFFu, left >= HK);
+          // The weights at once, against the maximum so far; in the rare step that
+          // raises it (2^15 and more above, or the first keys of a row) once more
+          // from the scores, which still stand in TMEM.
+          uint32_t p[HK / 2];
+          for (int tries = 0; tries < 2; ++tries) {
+            float mx;
+            const float more = whole ? weigh<HK, false>(from, sc, fac, top, left, p, mx)
+                                     : weigh<HK, true>(from, sc, fac, top, left, p, mx);
+            const bool raise = mx > kRaise || (none && mx > -INFINITY);
+            if (tries > 0 || !__any_sync(0xFFFFFFFFu, raise)) {
+              sum += more;
+              break;
+            }
+            const float up = raise ? mx : 0.0f;
+            const float f = none ? 1.0f : ex2(-up);  // nothing to rescale before the first key
+            top += up;
+            if (raise) none = false;
+            sum *= f;
+            if (hf == 1) {  // the first half's products must have been added
+              wait_bounded(bar(HALF + w), ph, abort_flag, a.status);
+              __syncwarp();
+              tc_fence_after();
+            }
+            if (t > 0 || hf > 0) {  // the sum so far stands in TMEM, and no product is under way
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tmem_row + kColO + c, o);
+                wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(tmem_row + kColO + c, o);
+              }
             }
           }
+          tmem_st32(tmem_row + kColS + 32 * hf, p);
+          wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(P_FULL + 2 * w + hf));
         }
-        tmem_st32(tmem_row + kColS + 64 * buf, p);
-        wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(P_FULL + 2 * w + buf));
       }
       row_stat[tid] = make_float2(none && sum == sum ? -INFINITY : top, sum);  // (a NaN query's piece counts)
     }
@@ -857,10 +870,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
       }
     } else if (whole_item && turned) {
-      for (int c = tid - 256; c < D * LPR; c += kThreads - 256) {
+      for (int c = tid - 256; c < D * LPR; c += 160) {
         const uint4 w = turn_chunk<true>(inv, c / LPR, c % LPR, a.r.h, one);
-        sts128(base + S::kMatrixOut + ((c % LPR) >> 3) * (D * 128) + (c / LPR) * 128 + (((c & 7) ^ (c / LPR & 7)) << 4), w.x, w.y,
-               w.z, w.w);
+        sts128(base + S::kMatrix + ((c % LPR) >> 3) * (D * 128) + (c / LPR) * 128 + (((c & 7) ^ (c / LPR & 7)) << 4), w.x, w.y, w.z,
+               w.w);
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -868,21 +881,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     __syncthreads();
     tc_fence_after();
     if (whole_item && turned) {
-      if (warp >= 14) {
-        const int w = warp - 14;
+      if (warp == 12) {
         if (elect_one()) {
-          const uint64_t md = desc_sw128(base + S::kMatrixOut);
-          if (w < tiles) {
+          const uint64_t md = desc_sw128(base + S::kMatrix);
 #pragma unroll
-            for (int term = 0; term < 2; ++term) {
-              const uint64_t od = desc_sw128(base + (term == 0 ? S::kQuery + w * S::kTileQ : w ? S::kSumLow1 : S::kSumLow0));
+          for (int w = 0; w < 2; ++w) {
+            if (w < tiles) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_ss(tmem + kColS + 128 * w, od + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
-                       md + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), idesc_of<T, D>(), term > 0 || k > 0);
+              for (int term = 0; term < 2; ++term) {
+                const uint64_t od = desc_sw128(base + (term == 0 ? S::kQuery + w * S::kTileQ : w ? S::kSumLow1 : S::kSumLow0));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                  mma_ss(tmem + kColS + 128 * w, od + (uint64_t)((k >> 2) * (kTileRows * 8) + (k & 3) * 2),
+                         md + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), idesc_of<T, D>(), term > 0 || k > 0);
+              }
             }
+            commit(bar(TURN + w));
           }
-          commit(bar(TURN + w));
         }
         __syncwarp();
       } else if (warp < 8) {
@@ -937,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     steps += take;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      tile_phase[w][0] += (tile_take[w] + 1) >> 1, tile_phase[w][1] += tile_take[w] >> 1;
+      tile_steps[w] += tile_take[w];
       tile_items[w] += tile_take[w] > 0;
     }
   }
@@ -946,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 14)
+  if (warp == 12)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
 }
 

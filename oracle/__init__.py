@@ -27,6 +27,8 @@ Module map:
 * ``codebook``    -- f_d and the Lloyd-Max codebook by numerical integration.
 * ``quantize``    -- norm, normalise, brute-force nearest centroid, packing.
 * ``linear``      -- the quantized linear layer as an fp64 sum.
+* ``cache``       -- rotary positions over several axes, the 8-bit paged cache and
+  attention over it, by definition (no page prints these; closed forms pin them).
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against closed forms, printed values or brute force, except the pages'

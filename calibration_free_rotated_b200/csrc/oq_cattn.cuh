@@ -106,17 +106,20 @@ struct Share {
   long long into;         // units of that sequence before it
 };
 
-// All THREADS threads of the CTA take part and get the same answer.
-template <int RT, int TILE, int START, int THREADS>
+// All THREADS threads of the CTA take part and get the same answer.  SPARE: units that a
+// share may grow by when that leaves no item cut.
+template <int RT, int TILE, int START, int THREADS, int SPARE = 0>
 __device__ Share find_share(const Args& a, int cta, int ctas) {
   __shared__ long long warp_sum[THREADS / 32];
   __shared__ Share found;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (a.B <= 32) {  // each warp finds it for itself
     long long mine = 0;
+    unsigned item = 0;  // units of an item of the sequence, where all its items are alike
     if (lane < a.B) {
       const Seq s = load_seq(a, lane, cta == 0 && warp == 0);
       mine = units_before<RT, TILE, START>(a, s, row_tiles<RT>(s)) * a.c.heads;
+      if (SPARE > 0 && mine) item = (unsigned)units_before<RT, TILE, START>(a, s, 1);
     }
     long long incl = mine;
 #pragma unroll
@@ -127,6 +130,14 @@ __device__ Share find_share(const Args& a, int cta, int ctas) {
     Share s;
     s.total = __shfl_sync(0xFFFFFFFFu, incl, 31);
     s.size = (s.total + ctas - 1) / ctas;
+    if (SPARE > 0 && !a.causal) {  // whole items for each CTA, if they are all alike and cost little more
+      const unsigned most = __reduce_max_sync(0xFFFFFFFFu, item);
+      const unsigned least = __reduce_min_sync(0xFFFFFFFFu, item ? item : most);
+      if (most && most == least) {
+        const long long whole = (s.total / most + ctas - 1) / ctas * most;
+        if (whole <= s.size + SPARE) s.size = whole;
+      }
+    }
     const long long start = s.size * cta;
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, start >= incl - mine && start < incl);
     s.b = hit ? __ffs(hit) - 1 : a.B;

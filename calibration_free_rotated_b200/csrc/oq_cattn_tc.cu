@@ -21,17 +21,17 @@
 // matrix is written into the values' place when it is needed.  (Butterflies on the
 // 256 rows took 33 thousand clocks an item, a tenth of a long one.)
 //
-// What bounds it (4608 x 4608 rows, D = 128, 24 heads, bf16: 337 us, 775 TFLOP/s, in
-// calls one by one 345; 31200 + 1560 keys for 1560 rows, 12 heads: 390 and 418;
+// What bounds it (4608 x 4608 rows, D = 128, 24 heads, bf16: 317 us, 823 TFLOP/s, in
+// calls one by one 319; 31200 + 1560 keys for 1560 rows, 12 heads: 390 and 418;
 // chunks of up to 511 rows, D = 64, fp16, causal: 83): 64 keys take 2150 clocks, of which
 // the exponentials take 1024 (16 a clock), the tensor cores 1100, the issue slots
 // 50 to 60 %.  Without the exponentials the first example takes 5 % less, without the
 // expansion 12 %, without the weights altogether 15 %, with a quarter of the products
 // 3 %: no single part is left to mend.  An item's beginning and end take 25 thousand
-// clocks (D = 64: 15), a fifth of the first example.
-// Tried beside it (the first two examples, us): 64 keys a step, with scores a step
-// ahead, warps of their own for keys (2) and values (4), and a product warp for each
-// tile, 330 and 395 (one by one 346 and 427, the chunks 87); the same with four warps
+// clocks (D = 64: 15), a sixth of the first example.
+// Tried beside it (the first two examples, us, against 337 and 390 with cut items in
+// both): 64 keys a step, with scores a step ahead, warps of their own for keys (2) and
+// values (4), and a product warp for each tile, 330 and 395 (one by one 346 and 427, the chunks 87); the same with four warps
 // for keys and values, 335 and 449; with two threads a row (24 warps), 359 and 460;
 // this one with a product warp for each tile and six expanding warps, 371 and 447; two
 // CTAs an SM of one tile each, 1.9 times as long.
@@ -43,8 +43,8 @@
 //
 // fp16 queries keep a second term: the turn rounds them to 2^-12, which would
 // show beside an fp16 result, so what the first operand leaves out goes into a
-// second one and the scores take both.  (At D = 128 that operand's 32 KB leave
-// room for 64 keys a step instead of 128.)
+// second one and the scores take both.  (At D = 128 its 64 KB leave room for
+// one stage of values instead of two.)
 //
 // Every wait is bounded (~1 s); one that gives up records OQ_ERR_TIMEOUT and
 // raises a flag that lets all others return at once, and the CTA still reaches
@@ -64,6 +64,11 @@ using namespace cattn;
 constexpr int kThreads = 416, kRows = 256, kTileRows = 128;
 constexpr int kTmem = 512, kColS = 0, kColO = 256;  // a tile's columns begin 128 further on
 constexpr int kStart = 4;  // units of an item's beginning and end
+// A share may grow by kSpare units when that leaves no item cut: what a cut costs is another
+// beginning and end, the pieces' way through memory and the join.  4608 x 4608 rows, D =
+// 128, items cut or whole (us): 24 heads, 3 units more, 337 or 317; 23 heads, 8 units, 324 or
+// 320; 22 heads, 13 units, 321 or 329; 1200 x 1200 rows, 24 heads, 2 units, 61 or 51.
+constexpr int kSpare = 9;
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   }
   invert(a.r, inv, tid, D);
   const int cta = blockIdx.x;
-  const Share sh = find_share<kRows, KT, kStart, kThreads>(a, cta, gridDim.x);
+  const Share sh = find_share<kRows, KT, kStart, kThreads, kSpare>(a, cta, gridDim.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

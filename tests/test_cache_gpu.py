@@ -532,6 +532,10 @@ SPLITS = [  # new, past, heads, group, d, page, block, dtype, causal
     ([260, 1, 0, 520], [1000, 7, 0, 0], 3, 1, 128, 16, 128, "bf16", True),
     ([257, 255, 256], [31, 64, 0], 8, 1, 64, 64, 64, "bf16", True),
     ([30, 90] * 25, [40, 0] * 25, 3, 2, 64, 16, 64, "fp16", True),
+    # items that are all alike, a few for each CTA (one, two), none of them cut
+    ([257, 0, 257], [0, 0, 0], 30, 1, 64, 64, 64, "bf16", False),
+    ([300], [0], 75, 1, 64, 64, 64, "bf16", False),
+    ([129], [127], 37, 2, 128, 32, 128, "fp16", False),
 ]
 
 

@@ -11,9 +11,11 @@
 // Bound by memory (each value is read and written once).  A CTA takes a few
 // tokens and a share of the heads: its threads first put the tokens' cosines
 // and sines into shared memory (once for all heads), then each thread turns
-// pairs of 16-byte vectors.  (4608 tokens,
-// 48 heads of 128, bf16: 113 MB in 23 us, 4.9 TB/s; 32760 tokens, 24 heads, fp16:
-// 403 MB in 75 us, 5.4 TB/s; a batch's step of 64 tokens: 3 us, the launch's latency).
+// pairs of 16-byte vectors, two units under way at a time.  4608 tokens, 48 heads of
+// 128, bf16: 113 MB in 21 us, 5.3 TB/s; 32760 tokens, 24 heads, fp16: 403 MB in 68 us, 5.9
+// TB/s (halves: 20 and 64 us); a batch's step of 64 tokens: 2 us, the launch's latency.
+// (One unit at a time, neighbouring vectors and turns in plain order, read with four-way
+// bank conflicts: 26 and 77 us.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -66,86 +68,112 @@ struct Vec<float> {
   }
 };
 
+// Where pair p of a token has its turn: a thread's eight lanes' pieces lie 64 bytes apart,
+// so 16-byte pieces are swapped within 64 bytes, and the eight come from different banks.
+__device__ __forceinline__ int turn_at(int p) { return p ^ ((p >> 4 & 3) << 1); }
+
 // A row's 16-byte vectors in units of two: HALVES: unit u < pairs / N holds the
-// vectors N u and pairs + N u that turn into each other; otherwise, and for
-// what lies behind the turned part, two neighbouring vectors.  An odd vector at
-// the end stands alone (`two` false).
+// vectors N u and pairs + N u that turn into each other, the others what lies behind
+// the turned part, two neighbouring vectors; otherwise vector u and the one half a row
+// further on, so that lanes beside one another read what lies side by side.  An odd
+// vector at the end stands alone.  A thread has two units under way, the first two
+// while the token's turns are made.
 template <typename T, bool HALVES>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int vecs) {
-  constexpr int N = Vec<T>::N;
-  extern __shared__ float2 turns[];  // [tokens][pairs]
+  constexpr int N = Vec<T>::N, BATCH = 2;
+  extern __shared__ __align__(16) float2 turns[];  // [tokens][turn_at(pair)]
   chain();
   const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.T - t0);
   const int h0 = blockIdx.y * a.head_share, nh = min(a.head_share, a.heads - h0);
+  const int row_units = a.units, total = nt * nh * row_units, stride = (a.pairs + 7) & ~7;
+  const int first_pass = HALVES ? a.pairs / N : 0;  // units that pair two halves
+  uint4 w[BATCH][2];
+  int token[BATCH], unit[BATCH];
+  char* to[BATCH];
+  auto load = [&](int i, int k) {
+    const int row = row_units == 1 ? i : (int)__umulhi((unsigned)i, a.div_units);
+    const int u = i - row * row_units;
+    const int t = row / nh, h = row - t * nh;
+    const char* x = a.x + (t0 + t) * a.xt + (h0 + h) * a.xh;
+    to[k] = a.y + (t0 + t) * a.yt + (h0 + h) * a.yh;
+    token[k] = t, unit[k] = u;
+    const bool pass = HALVES && u < first_pass;
+    const int v0 = pass || !HALVES ? u : 2 * u, v1 = pass ? u + first_pass : HALVES ? v0 + 1 : u + row_units;
+    w[k][0] = *reinterpret_cast<const uint4*>(x + 16 * v0);
+    if (v1 < vecs) w[k][1] = *reinterpret_cast<const uint4*>(x + 16 * v1);
+  };
+#pragma unroll
+  for (int k = 0; k < BATCH; ++k)
+    if (threadIdx.x + k * kThreads < total) load(threadIdx.x + k * kThreads, k);
   for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
     const int t = i / a.pairs, p = i - t * a.pairs;
     const long long pos = a.pos[(size_t)(t0 + t) * a.n_axes + a.axis[p]];
     const unsigned long long turn = (unsigned long long)pos * a.freq[p];
     float s, c;
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
-    turns[i] = make_float2(c, a.inverse ? -s : s);
+    turns[t * stride + turn_at(p)] = make_float2(c, a.inverse ? -s : s);
   }
   __syncthreads();
-  const int row_units = a.units, total = nt * nh * row_units;
-  const int first_pass = HALVES ? a.pairs / N : 0;  // units that pair two halves
-  for (int i = threadIdx.x; i < total; i += kThreads) {
-    const int row = row_units == 1 ? i : (int)__umulhi((unsigned)i, a.div_units);
-    const int u = i - row * row_units;
-    const int t = row / nh, h = row - t * nh;
-    const char* x = a.x + (t0 + t) * a.xt + (h0 + h) * a.xh;
-    char* y = a.y + (t0 + t) * a.yt + (h0 + h) * a.yh;
-    const float2* cs = turns + t * a.pairs;
-    if (HALVES && u < first_pass) {
-      const uint4 w0 = *reinterpret_cast<const uint4*>(x + 16 * u);
-      const uint4 w1 = *reinterpret_cast<const uint4*>(x + 16 * (u + first_pass));
-      float p[N], q[N];
-      Vec<T>::load(w0, p);
-      Vec<T>::load(w1, q);
+  for (int i0 = threadIdx.x; i0 < total; i0 += BATCH * kThreads) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float2 r = cs[u * N + k];
-        const float b = q[k];
-        q[k] = fmaf(p[k], r.y, b * r.x);
-        p[k] = fmaf(p[k], r.x, -(b * r.y));
-      }
-      *reinterpret_cast<uint4*>(y + 16 * u) = Vec<T>::store(p);
-      *reinterpret_cast<uint4*>(y + 16 * (u + first_pass)) = Vec<T>::store(q);
-    } else {
-      const int v0 = 2 * first_pass + 2 * (u - first_pass);
-      const bool two = v0 + 1 < vecs;
-      uint4 w[2];
-      w[0] = *reinterpret_cast<const uint4*>(x + 16 * v0);
-      if (two) w[1] = *reinterpret_cast<const uint4*>(x + 16 * (v0 + 1));
+    for (int k = 0; k < BATCH; ++k) {
+      if (i0 + k * kThreads >= total) continue;
+      const int u = unit[k];
+      const float2* cs = turns + token[k] * stride;
+      char* y = to[k];
+      if (HALVES && u < first_pass) {
+        float p[N], q[N];
+        Vec<T>::load(w[k][0], p);
+        Vec<T>::load(w[k][1], q);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (j == 1 && !two) break;
-        const int p0 = (v0 + j) * (N / 2);
-        if (!HALVES && p0 < a.pairs) {  // the rest is carried over bit for bit
-          float p[N];
-          Vec<T>::load(w[j], p);
-          const uint4 as_is = w[j];
-#pragma unroll
-          for (int k = 0; k < N / 2; ++k) {
-            const float2 r = p0 + k < a.pairs ? cs[p0 + k] : make_float2(1.0f, 0.0f);
-            const float b = p[2 * k + 1];
-            p[2 * k + 1] = fmaf(p[2 * k], r.y, b * r.x);
-            p[2 * k] = fmaf(p[2 * k], r.x, -(b * r.y));
-          }
-          w[j] = Vec<T>::store(p);
-          if (p0 + N / 2 > a.pairs) {  // the turned part ends inside this vector
-            const uint32_t* old = &as_is.x;
-            uint32_t* now = &w[j].x;
-            constexpr int words = (int)(sizeof(T) / 2);  // words of a pair
-#pragma unroll
-            for (int k = 0; k < N / 2; ++k)
-#pragma unroll
-              for (int q = 0; q < words; ++q)
-                if (p0 + k >= a.pairs) now[k * words + q] = old[k * words + q];
-          }
+        for (int e = 0; e < N; e += 2) {
+          const float4 r = *reinterpret_cast<const float4*>(cs + turn_at(u * N + e));
+          const float b0 = q[e], b1 = q[e + 1];
+          q[e] = fmaf(p[e], r.y, b0 * r.x);
+          p[e] = fmaf(p[e], r.x, -(b0 * r.y));
+          q[e + 1] = fmaf(p[e + 1], r.w, b1 * r.z);
+          p[e + 1] = fmaf(p[e + 1], r.z, -(b1 * r.w));
         }
-        *reinterpret_cast<uint4*>(y + 16 * (v0 + j)) = w[j];
+        *reinterpret_cast<uint4*>(y + 16 * u) = Vec<T>::store(p);
+        *reinterpret_cast<uint4*>(y + 16 * (u + first_pass)) = Vec<T>::store(q);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int v = HALVES ? 2 * u + j : u + j * row_units;
+          if (v >= vecs) break;
+          const int p0 = v * (N / 2);
+          uint4 now4 = w[k][j];
+          if (!HALVES && p0 < a.pairs) {  // the rest is carried over bit for bit
+            float p[N];
+            Vec<T>::load(now4, p);
+#pragma unroll
+            for (int e = 0; e < N / 2; e += 2) {
+              const float4 r = *reinterpret_cast<const float4*>(cs + turn_at(p0 + e));
+              const float b0 = p[2 * e + 1], b1 = p[2 * e + 3];
+              p[2 * e + 1] = fmaf(p[2 * e], r.y, b0 * r.x);
+              p[2 * e] = fmaf(p[2 * e], r.x, -(b0 * r.y));
+              p[2 * e + 3] = fmaf(p[2 * e + 2], r.w, b1 * r.z);
+              p[2 * e + 2] = fmaf(p[2 * e + 2], r.z, -(b1 * r.w));
+            }
+            now4 = Vec<T>::store(p);
+            if (p0 + N / 2 > a.pairs) {  // the turned part ends inside this vector
+              const uint32_t* old = &w[k][j].x;
+              uint32_t* now = &now4.x;
+              constexpr int words = (int)(sizeof(T) / 2);  // words of a pair
+#pragma unroll
+              for (int e = 0; e < N / 2; ++e)
+#pragma unroll
+                for (int x = 0; x < words; ++x)
+                  if (p0 + e >= a.pairs) now[e * words + x] = old[e * words + x];
+            }
+          }
+          *reinterpret_cast<uint4*>(y + 16 * v) = now4;
+        }
       }
     }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+      if (i0 + (BATCH + k) * kThreads < total) load(i0 + (BATCH + k) * kThreads, k);
   }
 }
 
@@ -178,7 +206,7 @@ int launch_rope(const RopeCall& c) {
   shares = std::min(shares, std::min(c.heads, 65535));
   a.head_share = (c.heads + shares - 1) / shares;
   const dim3 grid((unsigned)blocks, (unsigned)((c.heads + a.head_share - 1) / a.head_share));
-  const size_t smem = sizeof(float2) * (size_t)a.tokens * a.pairs;
+  const size_t smem = sizeof(float2) * (size_t)a.tokens * ((a.pairs + 7) & ~7);
   auto go = [&](auto kern) { return launch_chained("rope", kern, grid, kThreads, smem, c.stream, a, vecs); };
   if (c.dtype == OQ_BF16) return c.halves ? go(rope_kernel<__nv_bfloat16, true>) : go(rope_kernel<__nv_bfloat16, false>);
   if (c.dtype == OQ_FP16) return c.halves ? go(rope_kernel<__half, true>) : go(rope_kernel<__half, false>);

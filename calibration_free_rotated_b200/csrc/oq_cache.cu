@@ -22,7 +22,7 @@
 // lane's own accumulators, and it ends with the same 16 coordinates of the turned
 // row: codes are read and written as they lie.  (With eight coordinates a lane and
 // butterflies by shuffles, four times as many instructions, the write took 54 us and
-// the read 42 us for 4608 tokens of 24 heads; now 49 us both, 85 MB each.)  What is left
+// the read 42 us for 4608 tokens of 24 heads; now 52 us both, 85 MB each.)  What is left
 // above the 26 us of the bytes: the instructions of the turn (half of the issue slots)
 // and, for the read, a page's scale before its codes; a step of 64 tokens waits for one
 // chain of loads (page, scale, old codes).

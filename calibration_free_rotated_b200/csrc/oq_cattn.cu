@@ -30,7 +30,7 @@
 // four warps of a CTA take turns over the tokens and put their sums together at
 // the end of an item.  Four CTAs fit an SM (three stages a warp), 128 KB of the
 // cache under way on each: 64 sequences of 100 to 8200 tokens, 8 heads, group 4: 548 MB in
-// 115 us, 4.8 TB/s; one of 131072 tokens: 269 MB in 57 us, 4.7 TB/s.  The median CTA
+// 109 us, 5.0 TB/s; one of 131072 tokens: 269 MB in 60 us, 4.5 TB/s.  The median CTA
 // is done after 85 % of that time; what is left is the unevenness of the memory's
 // service between SMs, since shares are equal and fixed, and 8 us of the join.
 #include <algorithm>

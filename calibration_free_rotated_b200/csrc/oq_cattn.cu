@@ -9,11 +9,12 @@
 // show, what the rounding leaves out is a second term), the codes are exact in
 // fp16, sums are fp32.
 //
-// The running maximum is taken over score + ev (logarithms to base 2), so the
-// weights p * 2^ev that go to fp16 are at most 2^15 and right to 2^-12 where they
-// matter, whatever the pages' scales; the softmax sum takes them back times
-// 2^-ev in fp32.  The maximum is raised only when a score passes it by 15: the
-// accumulators are rarely touched, and most tiles need no exchange at all.
+// The running reference is taken over score + ev (logarithms to base 2), so the
+// weights p * 2^ev that go to fp16 are at most 2^15.9, and right to 2^-12 down to
+// 2^-26 of the largest (see kShift), whatever the pages' scales; the softmax sum
+// takes them back times 2^-ev in fp32.  The reference is raised only when a weight
+// would pass 2^15.9: the accumulators are rarely touched, and most tiles need no
+// exchange at all.
 //
 // Tensor tiles m16n8k16 with the cache as the left operand: keys (tokens x D)
 // for the scores and transposed values (D x tokens) for the sum, eight query
@@ -354,9 +355,10 @@ step_kernel(const __grid_constant__ Args a) {
           float f[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float t = fmaxf(fmaxf(sc[n][j], sc[n][2 + j]), top[n][j]);
+            float t = fmaxf(sc[n][j], sc[n][2 + j]);
 #pragma unroll
             for (int m = 4; m <= 16; m <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, m));
+            t = fmaxf(t - kShift, top[n][j]);
             f[j] = t == -INFINITY ? 1.0f : ex2(top[n][j] - t);
             top[n][j] = t;
             sum[n][j] *= f[j];

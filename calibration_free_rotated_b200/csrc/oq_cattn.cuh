@@ -28,10 +28,17 @@ namespace cattn {
 
 using namespace cache;
 
-// A row's running maximum is raised when a weight would pass 2^15 (fp16 holds 65504):
-// the weights' relative rounding is the same anywhere below, and few steps then
-// have to rescale what is summed up.
-constexpr float kRaise = 15.0f;
+// Weights go to the products in fp16, beside a reference kept for each row and raised only
+// when a weight would pass 2^kRaise (fp16 holds 65504, 2^15.99), so few steps have to rescale
+// what is summed up.  A weight is right to 2^-12 of itself down to 2^-14 beside the reference,
+// and off by up to 2^-25 below (the softmax's sum takes the weights in fp32).  So that weights
+// far below a row's largest keep their bits, the reference, when it is raised, is set below
+// the largest score: kShift below in the step kernel.  In the chunk kernel a raise is dear
+// (4608 x 4608 rows whose scores spread by 3 to 5 nats: 320 us with the reference at the
+// largest score, 393, 415 and 424 with it 8, 10 and 12 below), so it asks 16 of the keys at
+// hand: up to kShift below, but no further than leaves their mean exponent kRoom below (326
+// us).  Where one key stands 17 nats and more above the others, they keep 7 bits each.
+constexpr float kShift = 12.0f, kRaise = 15.9f, kRoom = 16.0f;
 // Most CTAs that the workspace has pieces for (the kernels' residency on 148 SMs).
 constexpr int kStepCtas = 148 * 4, kChunkCtas = 148;
 

@@ -36,10 +36,10 @@
 // this one with a product warp for each tile and six expanding warps, 371 and 447; two
 // CTAs an SM of one tile each, 1.9 times as long.
 //
-// Scales: as in oq_cattn.cu the running maximum is taken over score + ev, so
+// Scales: as in oq_cattn.cu the running reference is taken over score + ev, so
 // the weights carry their page's value exponent; groups of 16 tokens (no page is
 // smaller) have their own.  The accumulator is rescaled only when a weight would
-// pass 2^15.
+// pass 2^15.9.
 //
 // fp16 queries keep a second term: the turn rounds them to 2^-12, which would
 // show beside an fp16 result, so what the first operand leaves out goes into a
@@ -287,6 +287,20 @@ __device__ __forceinline__ float weigh(uint32_t scores, const float4* sc, float 
 #pragma unroll
   for (int g = 1; g < KEYS / 16; ++g) mx = fmaxf(mx, most[g]);
   return sum;
+}
+
+// The mean exponent (score + ev - top) of those of 16 keys that the row sees; `none` if it
+// sees none.
+__device__ __forceinline__ float mean_exponent(uint32_t scores, const float4& sc, float fac, float top, int left, float none) {
+  uint32_t v[16];
+  tmem_ld16(scores, v);
+  wait_ld();
+  float sum = 0.0f;
+  const int seen = sc.x == 0.0f ? 0 : min(left, 16);  // an empty page has none
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < seen) sum += fmaf(__uint_as_float(v[j]), sc.x * fac, sc.y - top);
+  return seen > 0 ? sum / (float)seen : none;
 }
 
 // A block Hadamard matrix's column in the rows' order: coordinate pi(j) has j here,
@@ -759,8 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           const uint32_t from = tmem_row + kColS + HK * hf;
           const int left = lim - (tok0 + t * KT + HK * hf);  // keys of the half that the row may see
           const bool whole = __all_sync(0xFFFFFFFFu, left >= HK);
-          // The weights at once, against the maximum so far; in the rare step that
-          // raises it (2^15 and more above, or the first keys of a row) once more
+          // The weights at once, against the reference so far; in the rare step that
+          // raises it (a weight above 2^15.9, or the first keys of a row) once more
           // from the scores, which still stand in TMEM.
           uint32_t p[HK / 2];
           for (int tries = 0; tries < 2; ++tries) {
@@ -772,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               sum += more;
               break;
             }
-            const float up = raise ? mx : 0.0f;
+            const float mean = mean_exponent(from, sc[0], fac, top, left, mx);
+            const float up = raise ? fmaxf(mx - kShift, fminf(mx, mean + kRoom)) : 0.0f;
             const float f = none ? 1.0f : ex2(-up);  // nothing to rescale before the first key
             top += up;
             if (raise) none = false;

@@ -457,10 +457,14 @@ OQ_API int oq_cache_read(const oq_kvcache* cache, oq_rpbh_t r, void* K, void* V,
  *          oq_cache_attention_workspace_bytes(cache, T, B, heads); it keeps
  *          nothing between calls, and calls that overlap need one each.
  * Sums are fp32; queries and softmax weights go to the tensor cores in fp16
- * beside powers of two of their own.  Rows outside all sequences, and those of
- * a sequence whose numbers do not fit (device status), are left as they were;
- * a page out of range counts as empty (device status).  The same call gives
- * the same bits every time.  Errors as oq_cache_write. */
+ * beside powers of two of their own.  A weight (times its values' scale) is
+ * right to 2^-12 of itself down to 2^-14 of the row's largest; where the
+ * largest stands far above the keys beside it, down to 2^-26, and what lies
+ * lower is off by up to 2^-37 of the largest.
+ * Rows outside all sequences, and those of a sequence whose numbers do not fit
+ * (device status), are left as they were; a page out of range counts as empty
+ * (device status).  The same call gives the same bits every time.  Errors as
+ * oq_cache_write. */
 OQ_API size_t oq_cache_attention_workspace_bytes(const oq_kvcache* cache, int T, int B, int heads);
 OQ_API int oq_cache_attention(const oq_kvcache* cache, oq_rpbh_t r, const void* Q, long long q_token, long long q_head,
                               void* O, long long o_token, long long o_head, int dtype, int heads, int T,

@@ -752,3 +752,58 @@ def test_a_block_from_its_projection_on(oq):
             assert np.all(err <= bound + (2.0 ** -8 + 2.0 ** -20) * np.linalg.norm(want, axis=-1))
             full, _ = oc.attention(f64(q[sl]), seen_k[b], seen_v[b], True, d ** -0.5, None)
             assert np.linalg.norm(f64(o[sl]) - full) <= 0.05 * np.linalg.norm(full)
+
+
+# ------------------------------------------------- one key far above thousands of others
+LOUD = [  # rows, keys, d, page, dtype: row tiles of 8 and 16 rows, and of 256; long and short caches
+    (1, 4097, 64, 64, "fp16"), (1, 4097, 128, 16, "bf16"), (7, 900, 64, 32, "bf16"), (1, 60000, 64, 128, "fp16"),
+    (16, 4097, 128, 64, "fp16"), (40, 2100, 64, 16, "bf16"),
+    (64, 4097, 64, 64, "fp16"), (300, 2049, 128, 32, "bf16"), (129, 1025, 128, 128, "fp16"),
+]
+
+
+@pytest.mark.parametrize("gap", [12.0, 16.0, 17.5, 20.0])
+@pytest.mark.parametrize("n,keys,d,page,dt", LOUD)
+def test_attention_keys_far_below_the_loudest(oq, n, keys, d, page, dt, gap):
+    """The first key takes nearly all of the softmax and its value is 0, as a stream's first tokens
+    do: the output is what thousands of keys up to 20 nats lower leave.  Queries of equal magnitudes
+    are exact in fp16, so are the scores' integer sums; a weight is off by 2^-12 of itself (fp16),
+    and by 2^-16 for the exponent's fp32 roundings (scores below 64: 3 * 2^-24 * 64 ln 2) and
+    2^-22 of ex2; below 2^-14 it is off by up to 2^-25, where the largest stands at 2^12 or (more
+    than 48 rows) as high as leaves the mean exponent of 16 keys at -16, no higher than 2^12."""
+    rng = np.random.default_rng(keys + d)
+    unit = 0.5 / (12.0 * d ** 0.5)  # nats a code's step: the others' scores spread by 0.5
+    sign = rng.choice([-1.0, 1.0], d)
+    codes = rng.integers(-20, 21, (keys, d)).astype(np.int8)
+    codes[0] = np.rint(sign * gap / (unit * d))
+    assert np.abs(codes).max() <= 127
+    values = rng.integers(30, 128, (keys, d)).astype(np.int8)
+    values[0] = 0
+    pages = -(-keys // page)
+    order = rng.permutation(pages)
+    pad = lambda x: np.concatenate([x, np.zeros((pages * page - keys, d), np.int8)]).reshape(pages, 1, page, d)  # noqa: E731
+    cache = oq.KVCache(pages, 1, d, page)
+    for to, x in ((cache.k, codes), (cache.v, values)):
+        to[torch.from_numpy(order).cuda()] = torch.from_numpy(pad(x)).cuda()
+    cache.k_scale.fill_(2.0 ** -5)
+    cache.v_scale.fill_(2.0 ** -3)
+    part = 1.0 - rng.integers(0, 5, n) / 16  # a row's share of the gap
+    q = sign[None, None] * part[:, None, None]
+    q16 = torch.from_numpy(q).to(DT[dt]).cuda()
+    assert np.array_equal(f64(q16), q)
+    out = f64(oq.cache_attention(cache, q16, ints([0, n]), ints([keys]), ints(order[None]), causal=False, scale=32 * unit))
+    oq.device_status()
+    s = (q[:, 0] @ codes.T.astype(float)) * unit
+    p = np.exp(s - s.max(1, keepdims=True))
+    gap2 = (s[:, :16].max(1) - s[:, :16].mean(1)) / np.log(2)
+    low = 2.0 ** -(25 + (12 if n <= 48 else np.clip(gap2 - 16, 0, 12)[:, None]))  # beside the largest weight of 1
+    total, v = p.sum(1, keepdims=True), values.astype(float) / 8
+    want = (p / total) @ v
+    # each weight's own error, in the same direction for all, and the sum's
+    wrong = (np.minimum(p, (2.0 ** -12 + 2.0 ** -16) * p + low) / total) @ v + 2.0 ** -16 * want
+    err, size = np.linalg.norm(out[:, 0] - want, axis=1), np.linalg.norm(want, axis=1)
+    limit = np.linalg.norm(wrong, axis=1) + torch.finfo(DT[dt]).eps / 2 * 1.01 * size
+    if dt == "fp16":  # outputs below the type's normal numbers
+        limit += 2.0 ** -25 * d ** 0.5
+    assert np.all(limit[part == 1] < 0.02 * size[part == 1])  # the limit does say something
+    assert np.all(err <= limit), (err / limit).max()

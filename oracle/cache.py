@@ -88,13 +88,35 @@ def gather(codes, scale, seq_table, n):
     return out
 
 
-def attention(q, k, v, causal, scale, rot, empty=None):
+def lost_weights(p, vv, shift, step=None):
+    """Bound, for each coordinate, of what the sum of p_j v_j loses below fp16's
+    normal numbers.  A weight p_j 2^ev_j beside the row's largest, which stands at
+    2^shift or above, is off by 2^-25 at most, and never by more than itself:
+    min(p_j |v_j|, 2^-(25 + shift) M |v_j| / 2^ev_j) with M the largest p_j 2^ev_j.
+    step: 2^ev_j; without it the values tell that codes are whole and at most 127:
+    |v_j| / 2^ev_j <= 127 |v_j| / max |v_j|, 2^ev_j <= the least |v_j| but 0 (a key
+    of nothing else: the largest of the others')."""
+    a = np.abs(vv)
+    if step is None:
+        code = 127 * a / np.maximum(a.max(1, keepdims=True), 1e-300)
+        step = np.where(a > 0, a, np.inf).min(1)
+        if not np.isfinite(step).any():
+            return np.zeros(vv.shape[1])
+        step = np.where(np.isfinite(step), step, step[np.isfinite(step)].max())
+    else:
+        code = a / step[:, None]
+    return np.minimum(p[:, None] * a, 2.0 ** -(25 + shift) * (p * step).max() * code).sum(0)
+
+
+def attention(q, k, v, causal, scale, rot, empty=None, shift=0, step=None):
     """One sequence: q [n, heads, d]; k, v [len, kv heads, d] in rotated
     coordinates; empty [len, kv heads]: keys that count as absent.  Returns the
     output, and for every row a bound of its error's 2-norm from queries and
     weights that are rounded to half a step of fp16 (2^-12 of each):
     a score is off by ds <= 2^-12 scale sum |q||k|, a weight by a factor
-    exp(+-2 max ds) (its own score and the sum) and by 2^-12."""
+    exp(+-2 max ds) (its own score and the sum) and by 2^-12, and by what weights
+    below fp16's normal numbers lose (lost_weights; shift: where a row's largest
+    weight stands at least, 2^shift; step [len, kv heads]: the values' scales)."""
     n, H, d = q.shape
     L, Hk, _ = k.shape
     u = turn(q, rot)
@@ -114,6 +136,6 @@ def attention(q, k, v, causal, scale, rot, empty=None):
             ds = abs(scale) * (np.abs(kk) @ (2.0 ** -12 * np.abs(u[i, h]) + 2.0 ** -25 * np.abs(u[i, h]).max()))
             rel = np.expm1(2 * ds[p > 1e-9].max()) + 2.0 ** -12 + 2.0 ** -18
             out[i, h] = turn_back((p @ vv)[None], rot)[0]
-            # weights below the fp16 range lose at most 2^-25 (of a weight of 1) each
-            bound[i, h] = rel * np.linalg.norm(p @ np.abs(vv)) + 2.0 ** -24 * np.linalg.norm(np.abs(vv).sum(0))
+            bound[i, h] = rel * np.linalg.norm(p @ np.abs(vv)) + np.linalg.norm(
+                lost_weights(p, vv, shift, None if step is None else step[:seen, kh][ok]))
     return out, bound

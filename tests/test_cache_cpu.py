@@ -203,3 +203,52 @@ def test_oracle_attention_and_rope():
         y = oc.rope(x, pos, [1.0, 0.1, 0.5], [0, 1, 1], halves)
         assert np.allclose(oc.rope(y, pos, [1.0, 0.1, 0.5], [0, 1, 1], halves, inverse=True), x)
         assert np.array_equal(y[..., 6:], x[..., 6:]) and np.array_equal(y[0], x[0])
+
+
+@pytest.mark.parametrize("gap,shift", [(9.0, 0), (12.0, 0), (12.0, 12), (16.0, 12), (17.5, 12), (18.0, 12)])
+def test_oracle_attention_bound_finds_lost_keys(gap, shift):
+    """One key far above thousands of others, its value 0: a sum without the others, or with their weights
+    rounded as they are beside a largest weight of 1, lies outside the bound; beside 2^shift, inside."""
+    rng = np.random.default_rng(2)
+    d, n = 64, 3000
+    q = rng.choice([-1.0, 1.0], (1, 1, d))
+    codes, values = rng.integers(-20, 21, (n, 1, d)).astype(float), rng.integers(30, 128, (n, 1, d)).astype(float)
+    unit = 0.5 / (12.0 * d ** 0.5)
+    codes[0] = np.rint(q[0] * gap / (unit * d))
+    values[0] = 0
+    want, bound = oc.attention(q, codes, values, False, unit, None, shift=shift, step=np.ones((n, 1)))
+    size = np.linalg.norm(want)
+    assert bound[0, 0] < 0.1 * size  # the bound does say something
+    s = unit * codes[:, 0] @ q[0, 0]
+    p = np.exp(s - s.max())
+
+    def off(weights):
+        return np.linalg.norm(weights @ values[:, 0] / p.sum() - want[0, 0])
+
+    assert off(p * (p == 1)) > 5 * bound[0, 0]
+    half = lambda c: (p * 2.0 ** c).astype(np.float16).astype(float) / 2.0 ** c  # noqa: E731
+    assert off(half(shift)) <= bound[0, 0]
+    if gap > 17:
+        assert off(half(0)) > 5 * bound[0, 0]
+
+
+def test_oracle_attention_bound_holds_for_scales_far_apart():
+    """Weights times their page's scale, rounded in fp16 beside the largest: always inside lost_weights' bound."""
+    rng = np.random.default_rng(3)
+    for _ in range(50):
+        n, d = int(rng.integers(1, 400)), 64
+        ev = np.repeat(rng.integers(-12, 13, -(-n // 16)), 16)[:n]
+        codes = rng.integers(-127, 128, (n, d)).astype(float) * (rng.random((n, 1)) < 0.9)
+        s = rng.standard_normal(n) * rng.choice([1.0, 5.0, 12.0])
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        w = p * 2.0 ** ev
+        c = int(rng.integers(0, 13))
+        w16 = (w / w.max() * 2.0 ** c).astype(np.float16).astype(float) / 2.0 ** c * w.max()
+        small = w16 * 2.0 ** c / w.max() < 2.0 ** -14
+        err = np.abs((small * (w16 - w)) @ codes)
+        vv = codes * 2.0 ** ev[:, None]
+        tight = oc.lost_weights(p, vv, c, 2.0 ** ev)
+        assert np.all(err <= tight * (1 + 1e-9) + 1e-300)
+        if np.abs(codes).any(1).all():  # (keys without a value tell nothing of their scale)
+            assert np.all(tight <= oc.lost_weights(p, vv, c) * (1 + 1e-9) + 1e-300)

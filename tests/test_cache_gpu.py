@@ -807,3 +807,34 @@ def test_attention_keys_far_below_the_loudest(oq, n, keys, d, page, dt, gap):
         limit += 2.0 ** -25 * d ** 0.5
     assert np.all(limit[part == 1] < 0.02 * size[part == 1])  # the limit does say something
     assert np.all(err <= limit), (err / limit).max()
+
+
+@pytest.mark.parametrize("n,dt", [(1, "bf16"), (12, "fp16"), (12, "bf16"), (60, "fp16"), (200, "bf16")])
+def test_attention_over_a_loud_first_token(oq, n, dt):
+    """The same through the rotation and the cache's write: a first token about 18 nats above 2000 others,
+    which it shares pages' scales with, its value near 0; held to the oracle's bound, itself a few per
+    cent of the output (the query's rounding in a score of 18 nats, in the worst case)."""
+    rng = np.random.default_rng(41)
+    r, rot = rotation(oq, 64, 64)
+    keys = 2000
+    bt = Batch(rng, [n], [keys - n], 32)
+    base = rng.standard_normal(64)
+    base *= 8 / np.linalg.norm(base)
+    k, v = 0.5 * rng.standard_normal((keys, 1, 64)), 1 + rng.standard_normal((keys, 1, 64))
+    k[0, 0], v[0, 0] = 18 / 8 * base, 0.01 * v[0, 0]
+    cache = oq.KVCache(bt.n_pages, 1, 64, 32)
+    dev = lambda x: torch.from_numpy(x).to(DT[dt]).cuda()  # noqa: E731
+    oq.cache_write(cache, dev(k), dev(v), ints([0, keys]), ints([0]), ints(bt.table), rpbh=r)
+    q = dev(base[None, None] + 0.1 * rng.standard_normal((n, 1, 64)))
+    out = f64(oq.cache_attention(cache, q, ints([0, n]), ints([keys]), ints(bt.table), rpbh=r, causal=False))
+    oq.device_status()
+    kc, vc = (oc.gather(c.cpu().numpy(), f64(s), bt.table[0], keys)
+              for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    step = f64(cache.v_scale)[bt.table[0][np.arange(keys) // 32]]
+    s16 = 0.125 * oc.turn(f64(q), rot)[:, 0] @ kc[:16, 0].T / np.log(2)
+    shift = 12 if n <= 48 else float(np.clip(s16.max(1) - s16.mean(1) - 16, 0, 12).min())
+    want, bound = oc.attention(f64(q), kc, vc, False, 0.125, rot, shift=shift, step=step)
+    size = np.linalg.norm(want, axis=-1)
+    limit = bound + torch.finfo(DT[dt]).eps / 2 * 1.01 * size + (2.0 ** -25 * 8 if dt == "fp16" else 0)
+    assert np.all(limit < 0.05 * size)
+    assert np.all(np.linalg.norm(out - want, axis=-1) <= limit)

@@ -248,6 +248,7 @@ int oq_cache_attention(const oq_kvcache* cache, oq_rpbh_t r, const void* Q, long
   if (int rc = check_batch(cache, dtype, T, cu, lens, B, table, width)) return rc;
   if (heads < 1 || heads % cache->heads != 0)
     return fail(OQ_ERR_ARG, "query heads (%d) must be a multiple of the cache's (%d)", heads, cache->heads);
+  if (heads > 65535) return fail(OQ_ERR_UNSUPPORTED, "query heads <= 65535 (got %d)", heads);
   if (!std::isfinite(scale)) return fail(OQ_ERR_ARG, "scale must be finite");
   if (T == 0 || B == 0) return OQ_OK;
   if ((long long)T * heads > kMost)

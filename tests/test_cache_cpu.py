@@ -252,3 +252,19 @@ def test_oracle_attention_bound_holds_for_scales_far_apart():
         assert np.all(err <= tight * (1 + 1e-9) + 1e-300)
         if np.abs(codes).any(1).all():  # (keys without a value tell nothing of their scale)
             assert np.all(tight <= oc.lost_weights(p, vv, c) * (1 + 1e-9) + 1e-300)
+
+
+def test_most_query_heads(oq):
+    """Query heads beyond 65535 are refused, also where one token's rows would fit: the units of causal
+    rows are counted with 2 * group * 128 in 32 bits."""
+    L, c = oq.lib(), struct(oq, heads=1)
+
+    def attn(heads, T=1, causal=1):
+        return L.oq_cache_attention(c, None, BASE, 64 * heads, 64, 2 * BASE, 64 * heads, 64, 0, heads, T, BASE, BASE, 1,
+                                    BASE, 1, causal, 1.0, BASE, 0, None)
+
+    for heads in (65536, 1 << 20, 1 << 24, 1 << 25, (1 << 31) - 1):
+        for causal in (0, 1):
+            assert code(oq, attn(heads, causal=causal), "heads") == oq.OQ_ERR_UNSUPPORTED
+    assert code(oq, attn(65535), "workspace") == oq.OQ_ERR_ARG  # as far as the next check
+    assert code(oq, attn(65536, T=0), "heads") == oq.OQ_ERR_UNSUPPORTED

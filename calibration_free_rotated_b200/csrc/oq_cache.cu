@@ -421,27 +421,38 @@ __global__ void __launch_bounds__(kThreads, 4) read_kernel(const __grid_constant
   const int t0 = (int)(blockIdx.x * (kThreads / 32) + warp) * 16;
   if (t0 >= a.T) return;  // (no barrier of the CTA below)
   const int h0 = blockIdx.y * a.heads_warp, h1 = min(h0 + a.heads_warp, a.c.heads);
-  // the sequence of the first row: how many end at or before it
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 128) {
-    int e[4];
+  // the sequence of the first row: how many end at or before it.  Sequences from the first
+  // on whose offsets fall or leave the tensor (`last`) are left out, so the ends that are
+  // counted rise.
+  const bool report = (blockIdx.x | blockIdx.y | blockIdx.z) == 0 && warp == 0;
+  int before = 0, last = a.B;
+  for (int b0 = 0; b0 < last; b0 += 128) {
+    int s[4], e[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int b = b0 + 32 * q + lane;
-      e[q] = b < a.B ? a.cu[b + 1] : 0x7FFFFFFF;
+      s[q] = b < a.B ? a.cu[b] : 0;
+      e[q] = b < a.B ? a.cu[b + 1] : a.T;
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (b0 + 32 * q < a.B) before += __popc(__ballot_sync(0xFFFFFFFFu, e[q] <= t0));
+    for (int q = 0; q < 4; ++q) {
+      if (b0 + 32 * q >= last) break;
+      const bool off = e[q] < s[q] || e[q] > a.T;
+      if (report && (off || s[q] < 0)) bad_index(a.status);
+      const uint32_t bad = __ballot_sync(0xFFFFFFFFu, off), ended = __ballot_sync(0xFFFFFFFFu, e[q] <= t0);
+      if (bad) last = b0 + 32 * q + __ffs(bad) - 1;
+      before += __popc(ended & ((bad & (0u - bad)) - 1u));  // (no bad one: all)
+    }
   }
   // row of codes (page * page size + place) of the lane's row, or -1; lanes 16.. stand for nothing
   int at = -1;
   if (lane < 16 && t0 + lane < a.T) {
     const int t = t0 + lane;
     int b = before;
-    while (b < a.B && a.cu[b + 1] <= t) ++b;
-    if (b < a.B && t >= a.cu[b]) {
-      const long long p = (long long)a.first[b] + (t - a.cu[b]);
+    while (b < last && a.cu[b + 1] <= t) ++b;
+    const int from = b < last ? a.cu[b] : -1;
+    if (from >= 0 && t >= from) {
+      const long long p = (long long)a.first[b] + (t - from);
       if (p >= 0 && p < (long long)a.width * a.c.page) {
         const int page = a.table[(size_t)b * a.width + (int)(p >> plog)];
         if (page >= 0 && page < a.c.n_pages) at = (page << plog) + ((int)p & (a.c.page - 1));

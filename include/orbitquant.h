@@ -423,9 +423,11 @@ typedef struct {
  * past   : device int32 [B], tokens that sequence b holds already (0: the page
  *          is taken as new); the new ones follow.
  * Two sequences must not write into one page.  A sequence whose numbers do not
- * fit (cu out of 0..T or decreasing, past negative, more than width * page
- * tokens) and a page outside 0..n_pages-1 are left out and reported in the
- * device status (OQ_ERR_ARG).
+ * fit (cu[b] or cu[b+1] out of 0..T, cu[b+1] < cu[b], past negative, more than
+ * width * page tokens) and a page outside 0..n_pages-1 are left out and reported
+ * in the device status (OQ_ERR_ARG).  Once cu decreases, what is done for the
+ * sequences behind that place, and to rows that they share with others, is not
+ * defined.
  * Errors: OQ_ERR_ARG (NULL, sizes, rotation of another width), OQ_ERR_ALIGN,
  * OQ_ERR_UNSUPPORTED (cache geometry, dtype, composed rotation). */
 OQ_API int oq_cache_write(const oq_kvcache* cache, oq_rpbh_t r, const void* K, long long k_token, long long k_head,
@@ -435,8 +437,10 @@ OQ_API int oq_cache_write(const oq_kvcache* cache, oq_rpbh_t r, const void* K, l
 /* Reads values back: row cu[b] + i is token first[b] + i of sequence b,
  *   x = Pi^T (code * scale), rounded once to dtype.
  * K, V   : device [T][heads][d] contiguous, OQ_BF16 or OQ_FP16.  Rows outside
- *          all sequences, and rows whose place is out of range (reported in the
- *          device status), are left as they were.
+ *          all sequences, those of a sequence whose cu does not fit and those
+ *          behind the first cu that decreases, and rows whose place is out of
+ *          range are left as they were (the last three reported in the device
+ *          status).
  * Arguments and errors otherwise as oq_cache_write. */
 OQ_API int oq_cache_read(const oq_kvcache* cache, oq_rpbh_t r, void* K, void* V, int dtype, int T, const int32_t* cu,
                          const int32_t* first, int B, const int32_t* table, int width, void* stream);

@@ -838,3 +838,53 @@ def test_attention_over_a_loud_first_token(oq, n, dt):
     limit = bound + torch.finfo(DT[dt]).eps / 2 * 1.01 * size + (2.0 ** -25 * 8 if dt == "fp16" else 0)
     assert np.all(limit < 0.05 * size)
     assert np.all(np.linalg.norm(out - want, axis=-1) <= limit)
+
+
+def test_read_leaves_out_sequences_that_do_not_fit(oq):
+    """Offsets that fall or leave 0..T: the read serves the sequences before, leaves the others' rows
+    as they were and reports them, as the write does."""
+    rng = np.random.default_rng(51)
+    d, heads, P, B, T = 64, 2, 16, 200, 600
+    new = [3] * B
+    cache = oq.KVCache(B, heads, d, P)
+    x = rows(rng, (T, heads, d), "bf16")
+    table = ints(rng.permutation(B)[:, None])
+    oq.cache_write(cache, x, x, ints(cum(new)), ints([0] * B), table)
+    for at in ([0, 1, 2], [31, 32, 33], [127, 128, 129, 198], [5, 150]):
+        good = cum(new)
+        whole, _ = oq.cache_read(cache, ints(good), ints([0] * B), table, T=T)
+        oq.device_status()
+        for kind in ("falls", "falls far", "ends behind T", "begins before 0"):
+            cu, served = list(good), np.ones(T, bool)
+            if kind == "falls":
+                b = at[0]
+                cu[b + 1] = cu[b] - 1
+                served[good[b]:] = False
+            elif kind == "falls far":
+                b = at[-1]
+                cu[b + 1] = 0
+                served[good[b]:] = False
+            elif kind == "ends behind T":  # the last sequences, all beyond the tensor
+                b = at[-1]
+                cu[b + 1:] = [T + 1 + i for i in range(B - b)]
+                served[good[b]:] = False
+            else:
+                b = at[0]
+                cu[:b + 1] = [-5] * (b + 1)
+                served[:good[b + 1]] = False
+            out = [torch.full((T, heads, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            oq.cache_read(cache, ints(cu), ints([0] * B), table, k=out[0], v=out[1])
+            with pytest.raises(oq.OQError) as e:
+                oq.device_status()
+            assert e.value.code == oq.OQ_ERR_ARG
+            oq.device_status()
+            for o in out:
+                keep = torch.from_numpy(served).cuda()
+                assert torch.equal(o[keep], whole[keep]), (kind, at)
+                assert torch.all(o[~keep] == 7.0), (kind, at)
+    # the offsets of the write's test: nothing of sequences 1 to 3
+    out = torch.full((8, heads, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    oq.cache_read(cache, ints([0, 2, 1, 3, 9]), ints([0] * 4), ints([[0], [1], [2], [3]]), k=out, v=out.clone())
+    with pytest.raises(oq.OQError):
+        oq.device_status()
+    assert not torch.any(out[:2] == 5.0) and torch.all(out[2:] == 5.0)

@@ -416,8 +416,10 @@ typedef struct {
  * than one step of the scale that stands, however the tokens were portioned.
  * Codes are decided in fp32: one may differ from the exact value's only where
  * u / 2^e lies within 1e-3 of the border between two codes.
- * K, V   : device [T][heads][d], OQ_BF16 or OQ_FP16, finite values (a NaN is
- *          stored as 0, an infinity saturates).
+ * K, V   : device [T][heads][d], OQ_BF16 or OQ_FP16, finite values.  A NaN of u
+ *          is stored as 0, an infinity saturates: what is not finite in x comes
+ *          to all coordinates of its block of the rotation, and to no others
+ *          (nor do sums of a block that pass fp32's range).
  * cu     : device int32 [B + 1], the new tokens of sequence b are rows cu[b] ..
  *          cu[b+1] - 1; rows outside all sequences are not read.
  * past   : device int32 [B], tokens that sequence b holds already (0: the page

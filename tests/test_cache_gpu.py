@@ -888,3 +888,43 @@ def test_read_leaves_out_sequences_that_do_not_fit(oq):
     with pytest.raises(oq.OQError):
         oq.device_status()
     assert not torch.any(out[:2] == 5.0) and torch.all(out[2:] == 5.0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,block", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (64, 0)])
+def test_write_keeps_what_is_not_finite_in_its_block(oq, d, block, dt):
+    """A NaN or an infinity reaches the coordinates of its own block of the rotation: those that come out
+    as NaN are stored as 0, as infinities saturate; the row's other blocks are written as u = Pi x says."""
+    rng = np.random.default_rng(61)
+    r, rot = rotation(oq, d, block)
+    perm = rot[0] if rot else np.arange(d)
+    heads, n = 2, 10
+    x = rng.standard_normal((n, heads, d))
+    at = [perm[0], perm[d // 2 + 1], perm[d - 1]]  # in the first block, in the middle, in the last
+    x[0, :, at[0]], x[1, :, at[1]], x[2, :, at[2]] = np.nan, np.nan, np.nan
+    x[3, :, at[0]], x[4, :, at[2]] = np.inf, -np.inf
+    x[5, :, perm[0]], x[5, :, perm[1]] = np.inf, np.inf  # meet with either sign
+    x[6, 0, at[1]], x[6, 1, at[0]] = np.nan, -np.inf     # other heads, other places
+    x[7, :, at[0]], x[7, :, at[2]] = np.inf, np.nan
+    x[8] = np.nan
+    x16 = torch.from_numpy(x).to(DT[dt]).cuda()
+    cache = oq.KVCache(n, heads, d, 16)
+    cache.k.fill_(77)
+    cache.v.fill_(77)
+    # a page for every row; keys as they are, values in the reversed order
+    oq.cache_write(cache, x16, x16.flip(0).contiguous(), ints(range(n + 1)), ints([0] * n), ints([[b] for b in range(n)]), rpbh=r)
+    oq.device_status()
+    with np.errstate(invalid="ignore"):
+        u = oc.turn(f64(x16), rot)
+    near = np.abs(u[9]) if rot is None else u[9]
+    assert np.isfinite(near).all()
+    for codes, scale, rows_u in ((cache.k, cache.k_scale, u), (cache.v, cache.v_scale, u[::-1])):
+        got, s = codes.cpu().numpy()[:, :, 0].astype(int), f64(scale)
+        for b in range(n):
+            for h in range(heads):
+                w = np.where(np.isnan(rows_u[b, h]), 0, rows_u[b, h])
+                e = oc.step_exponent(np.abs(w).max())
+                assert s[b, h] == 2.0 ** e
+                t = np.clip(w / 2.0 ** e, -127, 127)
+                off = np.abs(got[b, h] - np.rint(t))
+                assert off.max() <= 1 and np.all((off == 0) | (np.abs(t - np.floor(t) - 0.5) < 1e-3)), (b, h)

@@ -542,7 +542,10 @@ int launch_cattn(const AttnCall& c) {
   a.piece = static_cast<float*>(c.workspace);
   a.stat = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d));
   a.desc = reinterpret_cast<int4*>(static_cast<char*>(c.workspace) + piece_bytes(p, v->d) + stat_bytes(p));
-  if (p.rows == 256) return launch_cattn_chunk(a, c.dtype, v->d, c.stream);
+  if (p.rows == 256) {
+    a.stall = take_test_stall(7);
+    return launch_cattn_chunk(a, c.dtype, v->d, c.stream);
+  }
 #define OQ_STEP(T, D, TWO) \
   return p.rows == 8 ? launch_step<T, D, 1, TWO>(a, p.ctas, c.stream) : launch_step<T, D, 2, TWO>(a, p.ctas, c.stream)
   if (c.dtype == OQ_BF16) {

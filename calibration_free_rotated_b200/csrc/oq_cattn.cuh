@@ -56,6 +56,7 @@ struct Args {
   float* stat;    // [2 ctas][rows of a tile][2]: maximum, sum
   int4* desc;     // [ctas]: (pieces, sequence, head, row tile)
   int B, T, width, group, causal;
+  int stall;           // test hook: the chunk kernel's keys are never handed over (the waits run out)
   unsigned div_group;  // 2^32 / group, rounded up (group > 1)
   float scale;    // of the scores, times log2(e)
 };

@@ -46,9 +46,9 @@
 // second one and the scores take both.  (At D = 128 its 64 KB leave room for
 // one stage of values instead of two.)
 //
-// Every wait is bounded (~1 s); one that gives up records OQ_ERR_TIMEOUT and
-// raises a flag that lets all others return at once, and the CTA still reaches
-// its end and frees its TMEM.
+// Every wait is bounded (~1 s); one that gives up records OQ_ERR_TIMEOUT and raises a flag
+// that lets all others return at once.  The CTA then leaves at its item's end, waits (bounded)
+// for its own products under way, and frees its TMEM.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -93,19 +93,22 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
   const unsigned long long t0 = global_ns();
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((i & 63u) == 0) {
-      if (*abort_flag) return;
-      if (global_ns() - t0 > kWaitLimitNs) {
-        atomicExch(status, OQ_ERR_TIMEOUT);
-        *abort_flag = 1;
-        return;
-      }
+    if (*abort_flag || mbar_try_wait(bar, parity)) return;
+    if ((i & 63u) == 0 && global_ns() - t0 > kWaitLimitNs) {
+      atomicExch(status, OQ_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return;
     }
   }
 }
 __device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
   if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, abort_flag, status);
+}
+// The last wait of a CTA, for its own products and arrivals under way, whether or not it gave up.
+__device__ __forceinline__ void wait_own(uint32_t bar) {
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, 0u) && global_ns() - t0 < kWaitLimitNs) {
+  }
 }
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::kBars + 164);
   auto bar = [&](int i) { return bars + 8u * i; };
   // of the two tiles (S_FULL + w) and of a tile's halves (P_FULL + 2 w + half)
-  constexpr int K_FULL = 0, K_EMPTY = 1, V_FULL = 2, V_EMPTY = 4, S_FULL = 6, P_FULL = 8, HALF = 12, O_FULL = 14, TURN = 16;
+  constexpr int K_FULL = 0, K_EMPTY = 1, V_FULL = 2, V_EMPTY = 4, S_FULL = 6, P_FULL = 8, HALF = 12, O_FULL = 14, TURN = 16, END = 18;
 
   if (tid == 0) {
     mbar_init(bar(K_FULL), 4), mbar_init(bar(K_EMPTY), 1);
@@ -382,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       mbar_init(bar(P_FULL + 2 * i), 4), mbar_init(bar(P_FULL + 2 * i + 1), 4);
       mbar_init(bar(TURN + i), 1);
     }
+    mbar_init(bar(END), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(K_FULL));
+        if (lane == 0 && !a.stall) mbar_arrive(bar(K_FULL));
         if (t + 1 < take && ct < KT / 16) load_scales(t + 1);
 
         const uint32_t st = it % VST;
@@ -968,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       }
     }
     if (first && !last) desc = make_int4((int)((item_end - 1) / sh.size) - cta + 1, b, h, qt);
-    __syncthreads();
+    if (__syncthreads_or(*abort_flag)) break;
     steps += take;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -978,6 +982,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   }
   chain_next();
   if (tid == 0) a.desc[cta] = desc;
+  if (warp == 12) {  // nothing may arrive in shared memory or TMEM that is given back
+    if (elect_one()) commit(bar(END));
+    __syncwarp();
+    wait_own(bar(END));
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -847,7 +847,8 @@ int oq_test_composed_tables(oq_rpbh_t r, int xch, uint16_t* gather, uint16_t* st
 
 int oq_test_stall_next(int kernel) {
   clear_error();
-  if (kernel < 0 || kernel > 2) return fail(OQ_ERR_ARG, "kernel must be 0 (disarm), 1 or 2 (got %d)", kernel);
+  if ((kernel < 0 || kernel > 2) && kernel != 7)
+    return fail(OQ_ERR_ARG, "kernel must be 0 (disarm), 1, 2 or 7 (got %d)", kernel);
   g_test_stall.store(kernel);
   return OQ_OK;
 }

@@ -94,11 +94,12 @@ OQ_API int oq_set_debug(int on);
 
 /* Test hook for the failure path: the next launch of kernel 1 (rotate +
  * quantize, one-round rotations) or kernel 2 (codebook GEMM), on any stream,
- * issues none of its bulk / tensor copies.  Its bounded waits then run out
- * (about 1 s), it records OQ_ERR_TIMEOUT in the device status word and every
- * CTA leaves through its normal teardown, so the context stays usable; the
- * launch's outputs are undefined.  kernel 0 disarms.  One launch consumes it.
- * Errors: OQ_ERR_ARG for a kernel outside 0..2. */
+ * issues none of its bulk / tensor copies; that of kernel 7 (attention over the
+ * cache for many query rows) never hands over its keys.  The bounded waits then
+ * run out (about 1 s), the kernel records OQ_ERR_TIMEOUT in the device status
+ * word and every CTA leaves through its normal teardown, so the context stays
+ * usable; the launch's outputs are undefined.  kernel 0 disarms.  One launch
+ * consumes it.  Errors: OQ_ERR_ARG for any other kernel. */
 OQ_API int oq_test_stall_next(int kernel);
 
 /* Test hook (host only, no device needed): the composed-rotation kernel's

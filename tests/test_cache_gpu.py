@@ -928,3 +928,38 @@ def test_write_keeps_what_is_not_finite_in_its_block(oq, d, block, dt):
                 t = np.clip(w / 2.0 ** e, -127, 127)
                 off = np.abs(got[b, h] - np.rint(t))
                 assert off.max() <= 1 and np.all((off == 0) | (np.abs(t - np.floor(t) - 0.5) < 1e-3)), (b, h)
+
+
+@pytest.mark.parametrize("new,past,heads,d,dt,block", [
+    ([130, 60], [300, 20], 2, 128, "bf16", 128),  # turned; two items with two tiles, two with one
+    ([200], [3000], 1, 64, "fp16", 0),            # not turned; items cut between CTAs, a join behind them
+    ([100], [0], 3, 128, "fp16", 64),             # one stage of values
+])
+def test_chunk_attention_wait_runs_out_and_context_survives(oq, new, past, heads, d, dt, block):
+    """The keys are never handed over, so the waits run out: the kernel reports it, frees what it holds
+    and leaves, and the next launch gives what it gave before.  Nothing traps or hangs."""
+    rng = np.random.default_rng(71)
+    r, _ = rotation(oq, d, block)
+    bt = Batch(rng, new, past, 64)
+    cache = filled(oq, rng, bt, heads, d, r, dt)
+    q = rows(rng, (bt.T, heads, d), dt)
+    args = (q, ints(bt.cu), ints(bt.total), ints(bt.table))
+    want = oq.cache_attention(cache, *args, rpbh=r)
+    step = oq.cache_attention(cache, q[:1], ints([0, 1]), ints([20]), args[3][:1], rpbh=r)
+    oq.device_status()
+    assert oq.lib().oq_test_stall_next(7) == oq.OQ_OK
+    # few rows go to another kernel, which does not consume it
+    assert torch.equal(step, oq.cache_attention(cache, q[:1], ints([0, 1]), ints([20]), args[3][:1], rpbh=r))
+    oq.device_status()
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    oq.cache_attention(cache, *args, rpbh=r)
+    end.record()
+    torch.cuda.synchronize()
+    with pytest.raises(oq.OQError) as e:
+        oq.device_status()
+    assert e.value.code == oq.OQ_ERR_TIMEOUT
+    assert 900 < begin.elapsed_time(end) < 5000  # one wait's limit, not one for each step
+    for _ in range(3):
+        assert torch.equal(want, oq.cache_attention(cache, *args, rpbh=r))
+    oq.device_status()

@@ -35,10 +35,11 @@ using namespace cache;
 // far below a row's largest keep their bits, the reference, when it is raised, is set below
 // the largest score: kShift below in the step kernel.  In the chunk kernel a raise is dear
 // (4608 x 4608 rows whose scores spread by 3 to 5 nats: 320 us with the reference at the
-// largest score, 393, 415 and 424 with it 8, 10 and 12 below), so it asks 16 of the keys at
-// hand: up to kShift below, but no further than leaves their mean exponent kRoom below (326
-// us).  Where one key stands 17 nats and more above the others, they keep 7 bits each.
-constexpr float kShift = 12.0f, kRaise = 15.9f, kRoom = 16.0f;
+// largest score, 393, 415 and 424 with it 8, 10 and 12 below), so it looks at the 64 keys at
+// hand: up to kShift below, but no further than leaves the weakest 16 of them, by their
+// largest, kRoom below.  Keys that spread as usual stay together and raise as seldom as
+// before; where a few stand 17 nats above the others, these keep 10 bits and more.
+constexpr float kShift = 12.0f, kRaise = 15.9f, kRoom = 10.0f;
 // Most CTAs that the workspace has pieces for (the kernels' residency on 148 SMs).
 constexpr int kStepCtas = 148 * 4, kChunkCtas = 148;
 

@@ -246,11 +246,11 @@ __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsig
 
 // A row's weights 2^(score + ev - top) of KEYS keys from its scores in TMEM, as
 // fp16 pairs, and into `sum` their part of the softmax's sum; `mx`: the largest
-// exponent.  sc: (key scale, ev, 2^-ev) of every 16 keys.  MASKED: only the first
+// exponent, `most`: that of every 16 keys.  sc: (key scale, ev, 2^-ev) of every 16 keys.  MASKED: only the first
 // `left` keys are seen.
 template <int KEYS, bool MASKED>
 __device__ __forceinline__ float weigh(uint32_t scores, const float4* sc, float fac, float top, int left,
-                                       uint32_t (&p)[KEYS / 2], float& mx) {
+                                       uint32_t (&p)[KEYS / 2], float (&most)[KEYS / 16], float& mx) {
   uint32_t v[KEYS];
 #pragma unroll
   for (int q = 0; q < KEYS / 32; ++q) tmem_ld32(scores + 32 * q, v + 32 * q);
@@ -258,7 +258,7 @@ __device__ __forceinline__ float weigh(uint32_t scores, const float4* sc, float 
 #pragma unroll
   for (int g = 0; g < KEYS / 16; ++g) s[g] = sc[g];
   wait_ld();
-  float most[KEYS / 16], sum = 0.0f;
+  float sum = 0.0f;
 #pragma unroll
   for (int g = 0; g < KEYS / 16; ++g) {
     const float c = s[g].x * fac, d = s[g].x != 0.0f ? s[g].y - top : -INFINITY;  // an empty page's scores go
@@ -290,20 +290,6 @@ __device__ __forceinline__ float weigh(uint32_t scores, const float4* sc, float 
 #pragma unroll
   for (int g = 1; g < KEYS / 16; ++g) mx = fmaxf(mx, most[g]);
   return sum;
-}
-
-// The mean exponent (score + ev - top) of those of 16 keys that the row sees; `none` if it
-// sees none.
-__device__ __forceinline__ float mean_exponent(uint32_t scores, const float4& sc, float fac, float top, int left, float none) {
-  uint32_t v[16];
-  tmem_ld16(scores, v);
-  wait_ld();
-  float sum = 0.0f;
-  const int seen = sc.x == 0.0f ? 0 : min(left, 16);  // an empty page has none
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (j < seen) sum += fmaf(__uint_as_float(v[j]), sc.x * fac, sc.y - top);
-  return seen > 0 ? sum / (float)seen : none;
 }
 
 // A block Hadamard matrix's column in the rows' order: coordinate pi(j) has j here,
@@ -782,16 +768,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           // from the scores, which still stand in TMEM.
           uint32_t p[HK / 2];
           for (int tries = 0; tries < 2; ++tries) {
-            float mx;
-            const float more = whole ? weigh<HK, false>(from, sc, fac, top, left, p, mx)
-                                     : weigh<HK, true>(from, sc, fac, top, left, p, mx);
+            float most[HK / 16], mx;
+            const float more = whole ? weigh<HK, false>(from, sc, fac, top, left, p, most, mx)
+                                     : weigh<HK, true>(from, sc, fac, top, left, p, most, mx);
             const bool raise = mx > kRaise || (none && mx > -INFINITY);
             if (tries > 0 || !__any_sync(0xFFFFFFFFu, raise)) {
               sum += more;
               break;
             }
-            const float mean = mean_exponent(from, sc[0], fac, top, left, mx);
-            const float up = raise ? fmaxf(mx - kShift, fminf(mx, mean + kRoom)) : 0.0f;
+            float low = mx;  // the least of the groups' largest exponents
+#pragma unroll
+            for (int g = 0; g < HK / 16; ++g) low = most[g] > -INFINITY ? fminf(low, most[g]) : low;
+            const float up = raise ? fmaxf(mx - kShift, fminf(mx, low + kRoom)) : 0.0f;
             const float f = none ? 1.0f : ex2(-up);  // nothing to rescale before the first key
             top += up;
             if (raise) none = false;

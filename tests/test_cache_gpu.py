@@ -770,7 +770,7 @@ def test_attention_keys_far_below_the_loudest(oq, n, keys, d, page, dt, gap):
     are exact in fp16, so are the scores' integer sums; a weight is off by 2^-12 of itself (fp16),
     and by 2^-16 for the exponent's fp32 roundings (scores below 64: 3 * 2^-24 * 64 ln 2) and
     2^-22 of ex2; below 2^-14 it is off by up to 2^-25, where the largest stands at 2^12 or (more
-    than 48 rows) as high as leaves the mean exponent of 16 keys at -16, no higher than 2^12."""
+    than 48 rows) as high as leaves the weakest 16 of 64 keys at 2^-10, no higher than 2^12."""
     rng = np.random.default_rng(keys + d)
     unit = 0.5 / (12.0 * d ** 0.5)  # nats a code's step: the others' scores spread by 0.5
     sign = rng.choice([-1.0, 1.0], d)
@@ -795,8 +795,8 @@ def test_attention_keys_far_below_the_loudest(oq, n, keys, d, page, dt, gap):
     oq.device_status()
     s = (q[:, 0] @ codes.T.astype(float)) * unit
     p = np.exp(s - s.max(1, keepdims=True))
-    gap2 = (s[:, :16].max(1) - s[:, :16].mean(1)) / np.log(2)
-    low = 2.0 ** -(25 + (12 if n <= 48 else np.clip(gap2 - 16, 0, 12)[:, None]))  # beside the largest weight of 1
+    gap2 = (s[:, :64].max(1) - s[:, :64].reshape(n, 4, 16).max(2).min(1)) / np.log(2)
+    low = 2.0 ** -(25 + (12 if n <= 48 else np.clip(gap2 - 10, 0, 12)[:, None]))  # beside the largest weight of 1
     total, v = p.sum(1, keepdims=True), values.astype(float) / 8
     want = (p / total) @ v
     # each weight's own error, in the same direction for all, and the sum's
@@ -831,8 +831,8 @@ def test_attention_over_a_loud_first_token(oq, n, dt):
     kc, vc = (oc.gather(c.cpu().numpy(), f64(s), bt.table[0], keys)
               for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
     step = f64(cache.v_scale)[bt.table[0][np.arange(keys) // 32]]
-    s16 = 0.125 * oc.turn(f64(q), rot)[:, 0] @ kc[:16, 0].T / np.log(2)
-    shift = 12 if n <= 48 else float(np.clip(s16.max(1) - s16.mean(1) - 16, 0, 12).min())
+    s64 = 0.125 * oc.turn(f64(q), rot)[:, 0] @ kc[:64, 0].T / np.log(2)
+    shift = 12 if n <= 48 else float(np.clip(s64.max(1) - s64.reshape(n, 4, 16).max(2).min(1) - 10, 0, 12).min())
     want, bound = oc.attention(f64(q), kc, vc, False, 0.125, rot, shift=shift, step=step)
     size = np.linalg.norm(want, axis=-1)
     limit = bound + torch.finfo(DT[dt]).eps / 2 * 1.01 * size + (2.0 ** -25 * 8 if dt == "fp16" else 0)

@@ -6,7 +6,7 @@
 // The angle is exact for far positions: f_p is held in turns per position as a
 // 64-bit fraction F = round(f_p / 2pi * 2^64), and pos * F mod 2^64 is the
 // turn's fraction with an error below |pos| * 2^-65, reduced without a float
-// division; its top 32 bits go through sincospif.
+// division; rounded to fp32 (a small angle keeps its 24 bits) it goes through sincospif.
 //
 // Bound by memory (each value is read and written once).  A CTA takes a few
 // tokens and a share of the heads: its threads first put the tokens' cosines
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const long long pos = a.pos[(size_t)(t0 + t) * a.n_axes + a.axis[p]];
     const unsigned long long turn = (unsigned long long)pos * a.freq[p];
     float s, c;
-    sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
+    sincospif((float)(long long)turn * 0x1p-63f, &s, &c);
     turns[t * stride + turn_at(p)] = make_float2(c, a.inverse ? -s : s);
   }
   __syncthreads();

@@ -963,3 +963,23 @@ def test_chunk_attention_wait_runs_out_and_context_survives(oq, new, past, heads
     for _ in range(3):
         assert torch.equal(want, oq.cache_attention(cache, *args, rpbh=r))
     oq.device_status()
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "halves"])
+def test_rope_small_angles(oq, layout):
+    """The sine of a small angle is right in itself, not only beside the cosine: 2^-24 for the angle's
+    float, 2 * 2^-23 for sincospif, and the fixed point's |pos| * 2^-65 turns."""
+    freq = [10.0 ** -(k / 2) for k in range(2, 18)]  # 0.1 down to 3e-9 radians a position
+    r = oq.Rope(freqs=freq, axes=[0] * 16, layout=layout)
+    pos = np.array([[1], [2], [-1], [-3], [17], [1000], [-70000], [0]])
+    x = torch.zeros((8, 1, 32), device="cuda")
+    i = np.arange(16)
+    a, b = (i, i + 16) if layout == "halves" else (2 * i, 2 * i + 1)
+    x[..., a] = 1.0
+    for inverse in (False, True):
+        y = f64(oq.rope_apply(r, x, ints(pos), inverse=inverse))[:, 0]
+        phi = pos * np.array(freq) * (-1 if inverse else 1)
+        slip = np.abs(pos) * 2.0 ** -65 * 2 * np.pi + np.abs(phi) * 2.0 ** -52
+        assert np.all(np.abs(y[:, b] - np.sin(phi)) <= (2.0 ** -22 + 2.0 ** -24) * 1.01 * np.abs(np.sin(phi))
+                      + slip + 2.0 ** -24 * np.abs(phi) * np.abs(np.cos(phi)))
+        assert np.all(np.abs(y[:, a] - np.cos(phi)) <= 2.0 ** -21)

@@ -102,9 +102,11 @@ __device__ __forceinline__ int row_tiles(const Seq& s) {
 template <int RT, int TILE, int START>
 __device__ __forceinline__ long long units_before(const Args& a, const Seq& s, int q) {
   if (!a.causal) return (long long)q * (START + max(1, (s.len + TILE - 1) / TILE));
-  const unsigned long long num = (unsigned long long)q * (2ull * a.group * max(0, s.len - s.n) + (unsigned long long)RT * (q + 1));
+  // floor(q (2 group (len - n) + RT (q + 1)) / (2 group TILE)), whose product would pass 64 bits
+  const unsigned long long past = (unsigned long long)q * (unsigned)max(0, s.len - s.n);
+  const unsigned long long rest = past % TILE * 2u * a.group + (unsigned long long)RT * q * (q + 1ull);
   const unsigned den = 2u * a.group * TILE;
-  const unsigned long long tiles = num >> 32 ? num / den : (unsigned)num / den;
+  const unsigned long long tiles = past / TILE + (rest >> 32 ? rest / den : (unsigned)rest / den);
   return (long long)q * (START + 1) + (long long)tiles;
 }
 

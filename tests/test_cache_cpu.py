@@ -268,3 +268,20 @@ def test_most_query_heads(oq):
             assert code(oq, attn(heads, causal=causal), "heads") == oq.OQ_ERR_UNSUPPORTED
     assert code(oq, attn(65535), "workspace") == oq.OQ_ERR_ARG  # as far as the next check
     assert code(oq, attn(65536, T=0), "heads") == oq.OQ_ERR_UNSUPPORTED
+
+
+def test_units_of_causal_rows_fit_64_bits():
+    """The kernels' count of the key tiles before row tile q, floor(q (2 g past + RT (q + 1)) / (2 g TILE)),
+    restated step by step: equal to the exact quotient over the sizes that are accepted, no step past 63
+    bits (the product itself passes 64 at 65535 heads on one, 2^15 new tokens behind 2^30)."""
+    most, rng = 0x7FFF0000, np.random.default_rng(4)
+    assert 2 ** 31 // 8 * (2 * 65535 * 2 ** 30) > 2 ** 64
+    for _ in range(20000):
+        tile, rt = int(rng.choice([64, 128])), int(rng.choice([8, 16, 256]))
+        g = int(2 ** rng.uniform(0, 16))
+        n = int(2 ** rng.uniform(0, np.log2(most // g)))
+        past, q = int(2 ** rng.uniform(0, 31)) % (most - n + 1), int(rng.integers(0, (n * g + rt - 1) // rt + 1))
+        first = q * past
+        rest = first % tile * 2 * g + rt * q * (q + 1)
+        assert first < 2 ** 63 and rest < 2 ** 63 and 2 * g * tile < 2 ** 32
+        assert first // tile + rest // (2 * g * tile) == q * (2 * g * past + rt * (q + 1)) // (2 * g * tile)

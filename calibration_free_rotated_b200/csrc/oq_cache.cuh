@@ -140,72 +140,48 @@ __device__ __forceinline__ int turn_at(const LaneTurn& t, int i) {
 }
 
 // Unnormalised Hadamard transform of every block of h coordinates (h = 32, 64
-// or 128; all lanes of the warp take part) of R rows, whose steps interleave.
-template <int R>
-__device__ __forceinline__ void fwht8(float (&x)[R][8], int l, int h) {
+// or 128; all lanes of the warp take part).
+__device__ __forceinline__ void fwht8(float (&x)[8], int l, int h) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int s = 1; s < 8; s <<= 1)
 #pragma unroll
-    for (int s = 1; s < 8; s <<= 1)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (!(i & s)) {
-          const float a = x[r][i], b = x[r][i + s];
-          x[r][i] = a + b;
-          x[r][i + s] = a - b;
-        }
+    for (int i = 0; i < 8; ++i)
+      if (!(i & s)) {
+        const float a = x[i], b = x[i + s];
+        x[i] = a + b;
+        x[i + s] = a - b;
+      }
 #pragma unroll
   for (int m = 1; m <= 8; m <<= 1) {
     if (8 * m < h) {
       const float sg = (l & m) ? -1.0f : 1.0f;
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[r][i] = fmaf(sg, x[r][i], __shfl_xor_sync(0xFFFFFFFFu, x[r][i], m));
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(sg, x[i], __shfl_xor_sync(0xFFFFFFFFu, x[i], m));
     }
   }
 }
 
-// u = Pi x of R rows, their 16-bit values standing STRIDE apart from `row` on
-// (shared memory, written by the rows' lanes before a __syncwarp).
-template <typename T, int R, int STRIDE>
-__device__ __forceinline__ void rotate_rows(const T* row, const LaneTurn& t, int l, const Rotation& rot, float (&x)[R][8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = turn_at(t, i);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float v = (float)row[r * STRIDE + at];
-      x[r][i] = (t.neg >> i & 1u) ? -v : v;
-    }
-  }
-  fwht8<R>(x, l, rot.h);
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[r][i] *= rot.norm;
-}
+// u = Pi x of the row of 16-bit values at `row` (shared memory, written by the row's
+// lanes before a __syncwarp).
 template <typename T>
 __device__ __forceinline__ void rotate_row(const T* row, const LaneTurn& t, int l, const Rotation& rot, float (&x)[8]) {
-  rotate_rows<T, 1, 0>(row, t, l, rot, reinterpret_cast<float(&)[1][8]>(x));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = (float)row[turn_at(t, i)];
+    x[i] = (t.neg >> i & 1u) ? -v : v;
+  }
+  fwht8(x, l, rot.h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= rot.norm;
 }
 
 // x = Pi^T u: the transposed turn scatters the values, rounded to T, into the
-// rows at `row` (shared memory; the rows' lanes read them after a __syncwarp).
-template <typename T, int R, int STRIDE>
-__device__ __forceinline__ void unrotate_rows(float (&x)[R][8], const LaneTurn& t, int l, const Rotation& rot, T* row) {
-  fwht8<R>(x, l, rot.h);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = turn_at(t, i);
-    const float f = (t.neg >> i & 1u) ? -rot.norm : rot.norm;
-#pragma unroll
-    for (int r = 0; r < R; ++r) row[r * STRIDE + at] = (T)(x[r][i] * f);
-  }
-}
+// row at `row` (shared memory; the row's lanes read it after a __syncwarp).
 template <typename T>
 __device__ __forceinline__ void unrotate_row(float (&x)[8], const LaneTurn& t, int l, const Rotation& rot, T* row) {
-  unrotate_rows<T, 1, 0>(reinterpret_cast<float(&)[1][8]>(x), t, l, rot, row);
+  fwht8(x, l, rot.h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) row[turn_at(t, i)] = (T)(x[i] * ((t.neg >> i & 1u) ? -rot.norm : rot.norm));
 }
 
 // Records that an index on the device (a page, a length) was out of range.

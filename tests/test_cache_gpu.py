@@ -983,3 +983,60 @@ def test_rope_small_angles(oq, layout):
         assert np.all(np.abs(y[:, b] - np.sin(phi)) <= (2.0 ** -22 + 2.0 ** -24) * 1.01 * np.abs(np.sin(phi))
                       + slip + 2.0 ** -24 * np.abs(phi) * np.abs(np.cos(phi)))
         assert np.all(np.abs(y[:, a] - np.cos(phi)) <= 2.0 ** -21)
+
+
+def test_offsets_beyond_32_bits(oq):
+    """Pages behind 2^32 bytes of codes, rows of a tensor 2^31 elements apart: the same bits as near ones."""
+    rng = np.random.default_rng(81)
+    heads, d, page = 8, 128, 128
+    n_pages = 2 ** 32 // (heads * page * d) + 8
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    codes = [torch.empty((n_pages, heads, page, d), dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.empty((n_pages, heads), dtype=torch.float32, device="cuda") for _ in range(2)]
+    cache = oq.KVCache.wrap(*codes, *scales)
+    r, _ = rotation(oq, d, 128)
+    k, v, q = (rows(rng, (300, n, d), "bf16") for n in (heads, heads, 2 * heads))
+    outs = []
+    for first in (0, n_pages - 3):
+        table = ints([[first + 2, first, first + 1]])
+        oq.cache_write(cache, k, v, ints([0, 300]), ints([0]), table, rpbh=r)
+        got = list(oq.cache_read(cache, ints([0, 300]), ints([0]), table, T=300, rpbh=r))
+        for n in (1, 9, 300):  # the three sizes of row tiles
+            got.append(oq.cache_attention(cache, q[:n], ints([0, n]), ints([300]), table, rpbh=r))
+        outs.append(got)
+    oq.device_status()
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and outs[0][0].any() and outs[0][4].any()
+    # a token's row every 2^27 elements of the same memory
+    far = codes[0].view(-1).view(torch.bfloat16).as_strided((17, 3, 64), (2 ** 27 - 64, 64, 1))
+    assert far.stride(0) * 16 >= 2 ** 31 - 2 ** 11
+    x = rows(rng, (17, 3, 64), "bf16")
+    far.copy_(x)
+    rope, pos = oq.Rope((16, 24, 24)), ints(rng.integers(0, 100, (17, 3)))
+    want = oq.rope_apply(rope, x, pos)
+    assert torch.equal(oq.rope_apply(rope, far, pos), want)
+    oq.rope_apply(rope, far, pos, out=far)
+    assert torch.equal(far, want)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_chunks_beyond_one_block(oq, causal):
+    """More sequences than the chunk kernel's CTA has threads, each with many rows; some empty."""
+    rng = np.random.default_rng(82)
+    r, rot = rotation(oq, 64, 64)
+    B = 450
+    new = [0 if b % 11 == 3 else int(rng.integers(50, 140)) for b in range(B)]
+    past = [int(n) for n in rng.integers(0, 40, B)]
+    assert sum(new) / B > 48
+    bt = Batch(rng, new, past, 16)
+    cache = filled(oq, rng, bt, 1, 64, r)
+    q = rows(rng, (bt.T, 1, 64), "bf16", loud=False)
+    out = oq.cache_attention(cache, q, ints(bt.cu), ints(bt.total), ints(bt.table), rpbh=r, causal=causal)
+    oq.device_status()
+    kc, vc = cache.k.cpu().numpy(), cache.v.cpu().numpy()
+    for b in [0, 1, 3, 200, 415, 416, 417, B - 1]:
+        k, v = (oc.gather(c, f64(s), bt.table[b], bt.total[b]) for c, s in ((kc, cache.k_scale), (vc, cache.v_scale)))
+        sl = slice(bt.cu[b], bt.cu[b + 1])
+        want, bound = oc.attention(f64(q[sl]), k, v, causal, 0.125, rot)
+        err = np.linalg.norm(f64(out[sl]) - want, axis=-1)
+        assert np.all(err <= bound + (2.0 ** -9 * 2 + 2.0 ** -20) * np.linalg.norm(want, axis=-1))

@@ -22,7 +22,7 @@
 // lane's own accumulators, and it ends with the same 16 coordinates of the turned
 // row: codes are read and written as they lie.  (With eight coordinates a lane and
 // butterflies by shuffles, four times as many instructions, the write took 54 us and
-// the read 42 us for 4608 tokens of 24 heads; now 52 us both, 85 MB each.)  What is left
+// the read 42 us for 4608 tokens of 24 heads; now 52 us both (51 in a graph), 85 MB each.)  What is left
 // above the 26 us of the bytes: the instructions of the turn (half of the issue slots)
 // and, for the read, a page's scale before its codes; a step of 64 tokens waits for one
 // chain of loads (page, scale, old codes).
@@ -217,7 +217,8 @@ __device__ __forceinline__ Place find_place(const WriteArgs& a, int unit, bool r
 // only where something is not finite, is held to the first one's registers; 4608 tokens of
 // 24 heads, written and read, 52.3 us against 50.9 without it, 53.7 if it were always taken.)
 template <typename T, int D, int WPU, int TURN>
-__global__ void __launch_bounds__(WPU < 4 ? 128 : 32 * WPU, TURN == 32 ? (D == 128 ? 5 : 8) / (WPU == 8 ? 2 : 1) : 0) write_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(WPU < 4 ? 128 : 32 * WPU, TURN == 32 ? (D == 128 ? 5 : 8) / (WPU == 8 ? 2 : 1) : 0)
+write_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int WARPS = WPU < 4 ? 4 : WPU, UNITS = WARPS / WPU, P = 16 * WPU;
   constexpr int KS = D / 16, PITCH = D + 4;  // words of a row pair in shared memory
   __shared__ __align__(16) uint32_t stage[WARPS][8 * PITCH];

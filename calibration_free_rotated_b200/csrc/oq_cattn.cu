@@ -14,7 +14,11 @@
 // 2^-26 of the largest (see kShift), whatever the pages' scales; the softmax sum
 // takes them back times 2^-ev in fp32.  The reference is raised only when a weight
 // would pass 2^15.9: the accumulators are rarely touched, and most tiles need no
-// exchange at all.
+// exchange at all.  (The running maximum and sum of a softmax in one pass: Milakov and
+// Gimelshein, 2018; raising the maximum past a threshold only is published too.)  Weights
+// of 2^-12 are a sixteenth of a bf16 result's rounding, but as much as an fp16 result's
+// own: fp16 results are off from the exact ones by 1.3 times as much as with fp32 weights
+// (2.8e-4 against 2.1e-4, chunks of D = 64).  A second term would double their products.
 //
 // Tensor tiles m16n8k16 with the cache as the left operand: keys (tokens x D)
 // for the scores and transposed values (D x tokens) for the sum, eight query
@@ -31,9 +35,10 @@
 // four warps of a CTA take turns over the tokens and put their sums together at
 // the end of an item.  Four CTAs fit an SM (three stages a warp), 128 KB of the
 // cache under way on each: 64 sequences of 100 to 8200 tokens, 8 heads, group 4: 548 MB in
-// 109 us, 5.0 TB/s; one of 131072 tokens: 269 MB in 60 us, 4.5 TB/s.  The median CTA
-// is done after 85 % of that time; what is left is the unevenness of the memory's
-// service between SMs, since shares are equal and fixed, and 8 us of the join.
+// 110 us inside a captured graph, 5.0 TB/s, and 119 us in calls one by one; one of 131072
+// tokens: 269 MB in 60 us, 4.5 TB/s, and 61.  The median CTA is done after 85 % of that
+// time; what is left is the unevenness of the memory's service between SMs, since shares
+// are equal and fixed, and 8 us of the join.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -94,7 +99,7 @@ struct Smem {
   static constexpr int kQ = kScales + kWarps * kStages * 8;         // [RT][D + 8] halves
   static constexpr int kLow = kQ + RT * (D + 8) * 2;                // the same: the query's second term
   static constexpr int kRow = kLow + (TWO ? RT * (D + 8) * 2 : 0);  // [RT] factor, [RT] limit, [RT] start of the scores
-  static constexpr int kStat = kRow + RT * 12;                      // [warps][RT] maximum, sum
+  static constexpr int kStat = kRow + RT * 12;                      // [warps][RT] reference, sum
   static constexpr int kStageRow = kStat + kWarps * RT * 8;         // [128 / (D / 8)][D] 16-bit rows
   static constexpr int kTotal = kStageRow + kThreads / (D / 8) * D * 2;
   static constexpr int kSumStride = D + 4;
@@ -467,7 +472,7 @@ step_kernel(const __grid_constant__ Args a) {
         float4* o = reinterpret_cast<float4*>(a.piece + (slot + r) * D + 8 * l);
         o[0] = make_float4(x[0], x[1], x[2], x[3]);
         o[1] = make_float4(x[4], x[5], x[6], x[7]);
-        if (l == 0)  // (a NaN query leaves no maximum; its piece must count all the same)
+        if (l == 0)  // (a NaN query leaves no reference; its piece must count all the same)
           *reinterpret_cast<float2*>(a.stat + 2 * (slot + r)) = make_float2(total == total ? mx : 0.0f, total);
       }
     }
@@ -490,6 +495,10 @@ Plan plan_of(int T, int B, int group) {
   //   rows    4            8           16           24           32           48
   //        28, 33, 81   31, 35, 81   46, 39, 81   62, 61, 82   78, 64, 82   105, 83, 83
   //                     33, 31, 71   46, 34, 71   61, 51, 71   75, 51, 71   105, 69, 72
+  // One choice for the call: where the sequences' rows lie on both sides of it, all pay for
+  // the average.  63 single tokens over 4000 keys beside a chunk of 4096, 32 heads on 8: 576
+  // us, and 106 and 249 in two calls; 127 beside a chunk of 1000: 416, and 191 and 54; with
+  // 24 heads on 24, 1126, and 265 and 191.  The header sends such batches in two calls.
   p.rows = per <= 8 ? 8 : per <= 48 ? 16 : 256;
   p.ctas = p.rows == 256 ? kChunkCtas : kStepCtas;
   return p;

@@ -14,7 +14,7 @@
 // no CTA walks over items that are not its own.
 //
 // An item that one CTA covers is finished there.  Of an item that is cut, each
-// CTA leaves a piece in the workspace (for each row its running maximum, sum and
+// CTA leaves a piece in the workspace (for each row its reference, sum and
 // weighted values, fp32): the CTA that has the first key tile in its slot 1, the
 // ones that go on with it in their slot 0.  The first also writes down which CTAs
 // hold pieces, and the joining kernel adds them up in the CTAs' order: no
@@ -54,7 +54,7 @@ struct Args {
   const int* table;
   int* status;
   float* piece;   // [2 ctas][rows of a tile][D]
-  float* stat;    // [2 ctas][rows of a tile][2]: maximum, sum
+  float* stat;    // [2 ctas][rows of a tile][2]: reference, sum
   int4* desc;     // [ctas]: (pieces, sequence, head, row tile)
   int B, T, width, group, causal;
   int stall;           // test hook: the chunk kernel's keys are never handed over (the waits run out)

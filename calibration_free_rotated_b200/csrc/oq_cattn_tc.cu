@@ -7,7 +7,7 @@
 //                128-byte-swizzled layout of the tensor cores' operands, once for
 //                both tiles: the keys as they lie, the values transposed by byte
 //                permutes, with the codes of what comes next already in registers.
-//   warps 0..7   four a tile, one thread a row: scores from TMEM, running maximum
+//   warps 0..7   four a tile, one thread a row: scores from TMEM, running reference
 //                and sum, weights back into TMEM in two halves, so that the first
 //                half's products run beside the second half's exponentials.
 //   warp 12      issues the products; one tile's run beside the other tile's
@@ -21,20 +21,24 @@
 // matrix is written into the values' place when it is needed.  (Butterflies on the
 // 256 rows took 33 thousand clocks an item, a tenth of a long one.)
 //
-// What bounds it (4608 x 4608 rows, D = 128, 24 heads, bf16: 317 us, 823 TFLOP/s, in
-// calls one by one 319; 31200 + 1560 keys for 1560 rows, 12 heads: 390 and 418;
-// chunks of up to 511 rows, D = 64, fp16, causal: 83): 64 keys take 2150 clocks, of which
-// the exponentials take 1024 (16 a clock), the tensor cores 1100, the issue slots
-// 50 to 60 %.  Without the exponentials the first example takes 5 % less, without the
-// expansion 12 %, without the weights altogether 15 %, with a quarter of the products
-// 3 %: no single part is left to mend.  An item's beginning and end take 25 thousand
-// clocks (D = 64: 15), a sixth of the first example.
+// What bounds it (4608 x 4608 rows, D = 128, 24 heads, bf16: 329 us, 794 TFLOP/s; 31200 +
+// 1560 keys for 1560 rows, 12 heads: 392 inside a captured graph and 414 to 428 in calls one by
+// one; chunks of up to 511 rows, D = 64, fp16, causal: 84): 64 keys take 2150 clocks, of which
+// the exponentials take 1024 (16 a clock), the tensor cores 1100, shared memory about as much
+// (a 128-key step moves 256 KB: the scores' operands 128, the values 64, the expanded codes
+// 64; at 128 bytes a clock 2048 of 4300 clocks), the issue slots 50 to 60 %.  Without the
+// exponentials the first example takes 5 % less, without the expansion 12 %, without the
+// weights altogether 15 %, with a quarter of the products 3 %: no single part holds it, but
+// scores and weights share their columns, so a tile's scores, weights, sum and next scores
+// follow one another.  An item's beginning and end take 25 thousand clocks (D = 64: 15), a
+// sixth of the first example; a sequence of at most 128 rows leaves the second tile idle.
 // Tried beside it (the first two examples, us, against 337 and 390 with cut items in
 // both): 64 keys a step, with scores a step ahead, warps of their own for keys (2) and
-// values (4), and a product warp for each tile, 330 and 395 (one by one 346 and 427, the chunks 87); the same with four warps
-// for keys and values, 335 and 449; with two threads a row (24 warps), 359 and 460;
-// this one with a product warp for each tile and six expanding warps, 371 and 447; two
-// CTAs an SM of one tile each, 1.9 times as long.
+// values (4), and a product warp for each tile, 330 and 395 (one by one 346 and 427, the chunks
+// 87); the same with four warps for keys and values, 335 and 449; with two threads a row (24
+// warps), 359 and 460; this one with a product warp for each tile and six expanding warps, 371
+// and 447; two CTAs an SM of one tile each, 1.9 times as long.  (Two row tiles in turn, one's
+// products beside the other's exponentials, is a published scheme for attention.)
 //
 // Scales: as in oq_cattn.cu the running reference is taken over score + ev, so
 // the weights carry their page's value exponent; groups of 16 tokens (no page is
@@ -63,11 +67,13 @@ using namespace cattn;
 
 constexpr int kThreads = 416, kRows = 256, kTileRows = 128;
 constexpr int kTmem = 512, kColS = 0, kColO = 256;  // a tile's columns begin 128 further on
-constexpr int kStart = 4;  // units of an item's beginning and end
+constexpr int kStart = 4;  // units of an item's beginning and end (at D = 128 it takes nearer to six)
 // A share may grow by kSpare units when that leaves no item cut: what a cut costs is another
 // beginning and end, the pieces' way through memory and the join.  4608 x 4608 rows, D =
 // 128, items cut or whole (us): 24 heads, 3 units more, 337 or 317; 23 heads, 8 units, 324 or
-// 320; 22 heads, 13 units, 321 or 329; 1200 x 1200 rows, 24 heads, 2 units, 61 or 51.
+// 320; 22 heads, 13 units, 321 or 329; 1200 x 1200 rows, 24 heads, 2 units, 61 or 51.  (Between
+// 8 and 13 units nothing was measured, nor shares of other lengths near the border; it is
+// asked for up to 32 sequences, whose items every warp sees at once.)
 constexpr int kSpare = 9;
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
@@ -331,7 +337,7 @@ struct Smem {
   static constexpr int kLow = kQuery + 2 * kTileQ;           // the queries' second term
   static constexpr int kScales = kLow + (TWO ? 2 * kTileQ : 0);             // [2][KT / 16] (key scale, ev, 2^-ev)
   static constexpr int kInverse = kScales + 2 * (KT / 16) * 16;             // [D] 16 bits: see invert
-  static constexpr int kStat = kInverse + 2 * D;                            // [rows] maximum, sum
+  static constexpr int kStat = kInverse + 2 * D;                            // [rows] reference, sum
   static constexpr int kBars = kStat + kRows * 8;
   static constexpr int kTotal = kBars + 192;
   static constexpr int kAlloc = kTotal + 1024;  // room to align the base
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       tc_fence_before();
       asm volatile("bar.sync 1, 288;" ::: "memory");
       float top = 0.0f, sum = 0.0f;
-      bool none = true;  // no key seen so far: the maximum says nothing
+      bool none = true;  // no key seen so far: the reference says nothing
       for (int t = 0; t < my_take; ++t) {
         const uint32_t ph = (my_steps + t) & 1u;
         wait_bounded(bar(S_FULL + w), ph, abort_flag, a.status);

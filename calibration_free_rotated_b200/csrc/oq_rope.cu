@@ -11,9 +11,10 @@
 // Bound by memory (each value is read and written once).  A CTA takes a few
 // tokens and a share of the heads: its threads first put the tokens' cosines
 // and sines into shared memory (once for all heads), then each thread turns
-// pairs of 16-byte vectors, two units under way at a time.  4608 tokens, 48 heads of
-// 128, bf16: 113 MB in 21 us, 5.3 TB/s; 32760 tokens, 24 heads, fp16: 403 MB in 68 us, 5.9
-// TB/s (halves: 20 and 64 us); a batch's step of 64 tokens: 2 us, the launch's latency.
+// pairs of 16-byte vectors, two units under way at a time.  Inside a captured graph: 4608
+// tokens, 48 heads of 128, bf16: 113 MB in 20.5 us, 5.5 TB/s; 32760 tokens, 24 heads, fp16:
+// 403 MB in 67 us, 6.0 TB/s (halves: 19 and 64 us); a batch's step of 64 tokens: 2 us, the
+// launch's latency.  In calls one by one 21.8, 73 and 6.5 us.
 // (One unit at a time, neighbouring vectors and turns in plain order, read with four-way
 // bank conflicts: 26 and 77 us.)
 #include <cuda_runtime.h>

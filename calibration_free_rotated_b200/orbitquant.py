@@ -475,7 +475,7 @@ def cache_read(cache: KVCache, cu: torch.Tensor, first: torch.Tensor, table: tor
                rpbh: Rpbh = None, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """Reads tokens first[b] .. of every sequence b back into rows cu[b] ..
     cu[b+1]-1 of k and v ([T, heads, d] contiguous; made as `dtype` if not
-    passed, with T rows)."""
+    passed, with T rows; rows outside all sequences then hold anything)."""
     if k is None or v is None:
         if k is not None or v is not None or T is None:
             raise ValueError("pass k and v, or T")
@@ -500,7 +500,10 @@ def cache_attention(cache: KVCache, q: torch.Tensor, cu: torch.Tensor, lens: tor
                     stream=None):
     """Attention of the rows q (cuda bf16 / fp16 [T, heads, d], rows cu[b] ..
     cu[b+1]-1 are sequence b's newest tokens) over the lens[b] tokens that the
-    sequence holds in the cache, these among them.  scale: 1/sqrt(d) if None."""
+    sequence holds in the cache, these among them.  scale: 1/sqrt(d) if None.
+    out: written and returned, rows outside all sequences as they were; a new
+    tensor if None, whose rows outside all sequences hold anything.  Single
+    tokens and long chunks are faster in two calls (oq_cache_attention)."""
     index, dtype = cache._index, q.dtype
     sq = _rows("q", q, index, None, cache.d)
     T, heads, d = q.shape

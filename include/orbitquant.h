@@ -461,13 +461,19 @@ OQ_API int oq_cache_read(const oq_kvcache* cache, oq_rpbh_t r, void* K, void* V,
  *          of them.  A row that sees none gives 0.
  * scale  : of the scores (1/sqrt(d) as a rule), finite.
  * workspace: device, 16-byte aligned, at least
- *          oq_cache_attention_workspace_bytes(cache, T, B, heads); it keeps
- *          nothing between calls, and calls that overlap need one each.
+ *          oq_cache_attention_workspace_bytes(cache, T, B, heads), which may be
+ *          more for a smaller B; it keeps nothing between calls, and calls
+ *          that overlap need one each.
  * Sums are fp32; queries and softmax weights go to the tensor cores in fp16
  * beside powers of two of their own.  A weight (times its values' scale) is
  * right to 2^-12 of itself down to 2^-14 of the row's largest; where the
  * largest stands far above the keys beside it, down to 2^-26, and what lies
- * lower is off by up to 2^-37 of the largest.
+ * lower is off by up to 2^-37 of the largest.  (fp16 results show it: they are
+ * off by 1.3 times as much as with fp32 weights; bf16 results hardly, whose
+ * queries are one fp16 term after the turn, those of fp16 two.)
+ * How the work is divided follows from T * heads / B, the average: a batch of
+ * single tokens beside long chunks takes 1.4 to 2.5 times as long as the single
+ * tokens and the chunks in two calls.
  * Rows outside all sequences, and those of a sequence whose numbers do not fit
  * (device status), are left as they were; a page out of range counts as empty
  * (device status).  The same call gives the same bits every time.  Errors as

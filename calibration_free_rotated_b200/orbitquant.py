@@ -370,12 +370,45 @@ class KVCache:
         for t in (k, v, k_scale, v_scale):
             if not t.is_contiguous() or t.device != k.device:
                 raise ValueError("cache tensors must be contiguous and on one device")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = (k, v, k_scale, v_scale)
         self.n_pages, self.heads, self.page, self.d = k.shape
         self.device, self._index = k.device, k.get_device()
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                     self.n_pages, self.heads, self.page, self.d)
         self._ref = ctypes.byref(self._struct)
+
+    # A tensor that is put in another's place is checked, and its address taken, like the first one.
+    @property
+    def k(self):
+        return self._tensors[0]
+
+    @k.setter
+    def k(self, t):
+        self._set(t, *self._tensors[1:])
+
+    @property
+    def v(self):
+        return self._tensors[1]
+
+    @v.setter
+    def v(self, t):
+        self._set(self._tensors[0], t, *self._tensors[2:])
+
+    @property
+    def k_scale(self):
+        return self._tensors[2]
+
+    @k_scale.setter
+    def k_scale(self, t):
+        self._set(*self._tensors[:2], t, self._tensors[3])
+
+    @property
+    def v_scale(self):
+        return self._tensors[3]
+
+    @v_scale.setter
+    def v_scale(self, t):
+        self._set(*self._tensors[:3], t)
 
 
 # The calls below are paced by the host where the work is small, so each looks at its

@@ -285,3 +285,21 @@ def test_units_of_causal_rows_fit_64_bits():
         rest = first % tile * 2 * g + rt * q * (q + 1)
         assert first < 2 ** 63 and rest < 2 ** 63 and 2 * g * tile < 2 ** 32
         assert first // tile + rest // (2 * g * tile) == q * (2 * g * past + rt * (q + 1)) // (2 * g * tile)
+
+
+def test_a_cache_follows_its_tensors(oq):
+    """A tensor that takes another's place is the one that the calls use (the first one's memory may be
+    handed on), and is checked as the first one was."""
+    c = oq.KVCache(3, 2, 64, 16, device="cpu")
+    for name in ("k", "v", "k_scale", "v_scale"):
+        new = getattr(c, name).clone()
+        setattr(c, name, new)
+        assert getattr(c, name) is new and getattr(c._struct, name) == new.data_ptr()
+        assert ctypes.cast(c._ref, ctypes.POINTER(oq._CacheStruct)).contents.d == 64
+        with pytest.raises(ValueError):
+            setattr(c, name, new[:2])
+        with pytest.raises(ValueError):
+            setattr(c, name, new.to(torch.float64))
+        assert getattr(c, name) is new and getattr(c._struct, name) == new.data_ptr()
+    c.k_scale *= 2  # in place: the same memory
+    assert c._struct.k_scale == c.k_scale.data_ptr()
